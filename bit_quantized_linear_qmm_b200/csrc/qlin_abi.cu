@@ -3,6 +3,7 @@
 // No exception crosses this file's functions; every failure is a qlin_status.
 #include <mutex>
 
+#include "adapters.cuh"
 #include "qlin_common.cuh"
 
 namespace qlin {
@@ -18,6 +19,13 @@ cudaError_t launch_quantize_int8_rows_dependent(const void* w, qlin_dtype w_dt, 
                                                 float* scale, cudaStream_t st, const DeviceInfo& dev);
 // k_tc_gemm.cu: the CTA tile of the int8 tcgen05 GEMM, mt sub-tiles of 128 tokens by bn columns.
 void tc_tile_shape(TcOp op, int64_t M, int64_t N, int64_t sms, int& mt, int& bn);
+
+// k_checkpoint.cu
+cudaError_t launch_dequantize_int8_groups(const int8_t* q, const float* scale, int64_t N, int64_t K, int g, void* out,
+                                          qlin_dtype o_dt, cudaStream_t st);
+cudaError_t launch_pergroup_wgrad(const void* dy, qlin_dtype dt, int64_t M, int64_t N, const int8_t* q,
+                                  const float* scale, int64_t K, int g, void* dw, void* db, cudaStream_t st,
+                                  const DeviceInfo& dev);
 
 namespace {
 
@@ -84,6 +92,44 @@ qlin_status from_cuda(cudaError_t e)
         return QLIN_OK;
     cudaGetLastError();  // clear a non-sticky launch error
     return e == cudaErrorNotSupported ? QLIN_ERR_UNSUPPORTED : QLIN_ERR_CUDA;
+}
+
+bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+bool int8_group_ok(int g) { return g == 64 || g == 128 || g == 256; }
+constexpr int64_t kMaxFeatures = 1 << 21;  // K, N of the adapter calls and of wgrad: block counts of a grid
+
+// Sizes of the adapter calls: INVALID_ARG below 1, UNSUPPORTED above what the kernels hold.
+qlin_status check_plan(int64_t M, int64_t L)
+{
+    if (M <= 0 || L <= 0)
+        return QLIN_ERR_INVALID_ARG;
+    return M <= kMaxPlanTokens && L <= kMaxAdapters ? QLIN_OK : QLIN_ERR_UNSUPPORTED;
+}
+qlin_status check_adapters(qlin_dtype dt, int64_t M, int64_t N, int64_t K, int64_t L, int64_t R, const void* plan,
+                           size_t plan_bytes)
+{
+    if (N <= 0 || K <= 0 || R <= 0)
+        return QLIN_ERR_INVALID_ARG;
+    const qlin_status s = check_plan(M, L);
+    if (s != QLIN_OK)
+        return s;
+    if (!dtype_ok(dt) || R > kMaxRank || N >= kMaxFeatures || K >= kMaxFeatures)
+        return QLIN_ERR_UNSUPPORTED;
+    if (plan_bytes < qlin_adapters_plan_size(M, L))
+        return QLIN_ERR_INVALID_ARG;
+    return aligned16(plan) ? QLIN_OK : QLIN_ERR_MISALIGNED;
+}
+
+// Every non-null pointer is a multiple of `bytes`.
+template <typename... P>
+bool aligned_to(size_t bytes, const P*... p)
+{
+    return (((reinterpret_cast<uintptr_t>(p) % bytes) | ...) == 0);
+}
+bool overlap(const void* p, size_t pn, const void* q, size_t qn)
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return p && q && a < b + qn && b < a + pn;
 }
 
 // Shape/type rules common to the affine-format calls.
@@ -514,6 +560,132 @@ qlin_status w4a8_linear(const void* x, qlin_dtype x_dt, int64_t M, int64_t K, co
                         void* stream)
 {
     return int_linear(TC_W4A8, x, x_dt, M, K, packed_w, scale_w, N, bias, y, workspace, ws_bytes, stream);
+}
+
+size_t qlin_adapters_plan_size(int64_t M, int64_t L)
+{
+    return check_plan(M, L) == QLIN_OK ? align256((size_t)plan_ints(M, L) * sizeof(int)) : 0;
+}
+
+qlin_status qlin_adapters_plan(const int32_t* ids, int64_t M, int64_t L, void* plan, size_t plan_bytes, void* stream)
+{
+    if (!ids || !plan)
+        return QLIN_ERR_INVALID_ARG;
+    qlin_status s = check_plan(M, L);
+    if (s != QLIN_OK)
+        return s;
+    if (plan_bytes < qlin_adapters_plan_size(M, L))
+        return QLIN_ERR_INVALID_ARG;
+    if (!aligned16(plan) || (reinterpret_cast<uintptr_t>(ids) & 3u) != 0)
+        return QLIN_ERR_MISALIGNED;
+    DeviceInfo dev;
+    if ((s = current_device(dev)) != QLIN_OK)
+        return s;
+    return from_cuda(launch_adapters_plan(ids, M, L, plan, static_cast<cudaStream_t>(stream)));
+}
+
+size_t qlin_adapters_workspace_size(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R, int)
+{
+    if (check_plan(M, L) != QLIN_OK || N <= 0 || K <= 0 || R <= 0 || R > kMaxRank || N >= kMaxFeatures ||
+        K >= kMaxFeatures)
+        return 0;
+    return align256(adapters_simt_workspace(M, N, K, R));
+}
+
+qlin_status qlin_adapters_forward(const void* x, qlin_dtype dt, int64_t M, int64_t K, const void* a, const void* b,
+                                  const float* scales, int64_t L, int64_t R, int64_t N, const void* plan,
+                                  size_t plan_bytes, const void* base, void* out, float* u, void* workspace,
+                                  size_t ws_bytes, void* stream)
+{
+    if (!x || !a || !b || !scales || !plan || !out)
+        return QLIN_ERR_INVALID_ARG;
+    qlin_status s = check_adapters(dt, M, N, K, L, R, plan, plan_bytes);
+    if (s != QLIN_OK)
+        return s;
+    const size_t e = dtype_size(dt), xn = M * K * e, on = M * N * e;
+    if (!aligned_to(e, x, a, b, base, out) || !aligned_to(4, scales, u))
+        return QLIN_ERR_MISALIGNED;
+    if (overlap(out, on, x, xn) || (base != out && overlap(out, on, base, on)) ||
+        overlap(u, (size_t)M * R * 4, out, on))
+        return QLIN_ERR_INVALID_ARG;
+    if (!workspace || ws_bytes < qlin_adapters_workspace_size(M, N, K, L, R, 0) || !aligned256(workspace))
+        return QLIN_ERR_WORKSPACE;
+    DeviceInfo dev;
+    if ((s = current_device(dev)) != QLIN_OK)
+        return s;
+    const AdapterFwdArgs f = {x, a, b, scales, base, out, u, dt, M, K, N, L, R, plan_view(plan, M, L), workspace};
+    return from_cuda(launch_adapters_forward_simt(f, static_cast<cudaStream_t>(stream)));
+}
+
+qlin_status qlin_adapters_backward(const void* dy, qlin_dtype dt, int64_t M, int64_t N, const void* a, const void* b,
+                                   const float* scales, int64_t L, int64_t R, int64_t K, const void* plan,
+                                   size_t plan_bytes, const float* u, const void* x, const int8_t* q,
+                                   const float* q_scale, int group_size, const void* dx_base, void* dx, void* da,
+                                   void* db, void* workspace, size_t ws_bytes, void* stream)
+{
+    if (!dy || !a || !b || !scales || !plan || !u || !da || !db || !x == !q || (q && !q_scale) || (dx_base && !dx))
+        return QLIN_ERR_INVALID_ARG;
+    qlin_status s = check_adapters(dt, M, N, K, L, R, plan, plan_bytes);
+    if (s != QLIN_OK)
+        return s;
+    if (q && !int8_group_ok(group_size))
+        return QLIN_ERR_UNSUPPORTED;
+    if (q && K % group_size != 0)
+        return QLIN_ERR_INVALID_ARG;
+    const size_t e = dtype_size(dt), xn = M * K * e, yn = M * N * e;
+    if (!aligned_to(e, dy, a, b, x, dx_base, dx, da, db) || !aligned_to(4, scales, u, q_scale))
+        return QLIN_ERR_MISALIGNED;
+    if (overlap(dx, xn, dy, yn) || overlap(dx, xn, x, xn) || overlap(dx, xn, q, (size_t)M * K) ||
+        (dx_base != dx && overlap(dx, xn, dx_base, xn)))
+        return QLIN_ERR_INVALID_ARG;
+    if (!workspace || ws_bytes < qlin_adapters_workspace_size(M, N, K, L, R, 1) || !aligned256(workspace))
+        return QLIN_ERR_WORKSPACE;
+    DeviceInfo dev;
+    if ((s = current_device(dev)) != QLIN_OK)
+        return s;
+    const AdapterBwdArgs g = {dy, a,  b,  scales, u,  x, q, q_scale, group_size, dx_base,
+                              dx, da, db, dt,     M,  K, N, L,       R,          plan_view(plan, M, L),
+                              workspace};
+    return from_cuda(launch_adapters_backward_simt(g, static_cast<cudaStream_t>(stream)));
+}
+
+qlin_status qlin_dequantize_int8_groups(const int8_t* q, const float* scale, int64_t N, int64_t K, int group_size,
+                                        void* out, qlin_dtype out_dt, void* stream)
+{
+    if (!q || !scale || !out || N <= 0 || K <= 0 || N > INT32_MAX || K > INT32_MAX)
+        return QLIN_ERR_INVALID_ARG;
+    if (!dtype_ok(out_dt) || !int8_group_ok(group_size))
+        return QLIN_ERR_UNSUPPORTED;
+    if (K % group_size != 0)
+        return QLIN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(out) || !aligned_to(4, scale))
+        return QLIN_ERR_MISALIGNED;
+    DeviceInfo dev;
+    qlin_status s;
+    if ((s = current_device(dev)) != QLIN_OK)
+        return s;
+    return from_cuda(launch_dequantize_int8_groups(q, scale, N, K, group_size, out, out_dt,
+                                                   static_cast<cudaStream_t>(stream)));
+}
+
+qlin_status pergroup_wgrad(const void* dy, qlin_dtype dt, int64_t M, int64_t N, const int8_t* q, const float* scale,
+                           int64_t K, int group_size, void* dw, void* db, void* stream)
+{
+    if (!dy || !q || !scale || !dw || M <= 0 || N <= 0 || K <= 0 || M > INT32_MAX)
+        return QLIN_ERR_INVALID_ARG;
+    if ((dt != QLIN_BF16 && dt != QLIN_F16) || !int8_group_ok(group_size) || N >= kMaxFeatures || K >= kMaxFeatures)
+        return QLIN_ERR_UNSUPPORTED;
+    if (K % group_size != 0)
+        return QLIN_ERR_INVALID_ARG;
+    if (N % 8 != 0 || !aligned16(dy) || !aligned16(q) || !aligned16(dw) || !aligned_to(4, scale) ||
+        !aligned_to(2, db))
+        return QLIN_ERR_MISALIGNED;
+    DeviceInfo dev;
+    qlin_status s;
+    if ((s = current_device(dev)) != QLIN_OK)
+        return s;
+    return from_cuda(launch_pergroup_wgrad(dy, dt, M, N, q, scale, K, group_size, dw, db,
+                                           static_cast<cudaStream_t>(stream), dev));
 }
 
 qlin_status qlin_selftest_wait_timeout(unsigned limit_us, void* stream)

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes as C
 import os
 import re
+from typing import NamedTuple
 
 import torch
 
@@ -80,6 +81,14 @@ def lib():
         "qlin_quantize_int8_groups": ([P, I, I64, I64, I, P, P, P], I),
         "qlin_quantize_weight_int8": ([P, I, I64, I64, C.c_double, P, P, P], I),
         "pergroup_linear": ([P, I, I64, I64, P, P, I64, I, P, P, P, SZ, P], I),
+        "qlin_adapters_plan_size": ([I64, I64], SZ),
+        "qlin_adapters_plan": ([P, I64, I64, P, SZ, P], I),
+        "qlin_adapters_workspace_size": ([I64, I64, I64, I64, I64, I], SZ),
+        "qlin_adapters_forward": ([P, I, I64, I64, P, P, P, I64, I64, I64, P, SZ, P, P, P, P, SZ, P], I),
+        "qlin_adapters_backward": ([P, I, I64, I64, P, P, P, I64, I64, I64, P, SZ, P, P, P, P, I, P, P, P, P, P, SZ,
+                                    P], I),
+        "qlin_dequantize_int8_groups": ([P, P, I64, I64, I, P, I, P], I),
+        "pergroup_wgrad": ([P, I, I64, I64, P, P, I64, I, P, P, P], I),
         "qlin_get_device_status": ([P], I),
         "qlin_selftest_wait_timeout": ([C.c_uint, P], I),
     }
@@ -306,3 +315,144 @@ def quantize_weight_int8(w, clip_percentile=None):
     _check(lib().qlin_quantize_weight_int8(_ptr(w), _dt(w), R, Cc, p, _ptr(q), _ptr(s), _stream(w.device)),
            "qlin_quantize_weight_int8")
     return q, s
+
+
+def _expect(device, dtype, **tensors):
+    """Each of name=(tensor or None, shape[, dtype]): a contiguous CUDA tensor on `device` of that shape and type."""
+    for name, (t, shape, *dt) in tensors.items():
+        if t is None:
+            continue
+        _cuda(t)
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+        if t.dtype != (dt[0] if dt else dtype):
+            raise TypeError(f"{name} has dtype {t.dtype}, not {dt[0] if dt else dtype}")
+
+
+def _workspace(workspace, need: int, device):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    _cuda(workspace)
+    if workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, not on {device}")
+    return workspace
+
+
+class AdapterPlan(NamedTuple):
+    """The tokens of a batch ordered by adapter (adapters_plan); good for every layer of the batch."""
+    buffer: torch.Tensor
+    tokens: int
+    adapters: int
+
+
+def adapters_plan(ids, adapters: int, out: AdapterPlan | None = None) -> AdapterPlan:
+    """Orders a batch's tokens by adapter.  ids: int32 [M], each token's adapter, outside 0 .. adapters-1 for none.
+
+    out: a plan of the same sizes to write again (a captured graph keeps the buffer it was captured with)."""
+    _cuda(ids)
+    if ids.dim() != 1 or ids.dtype != torch.int32:
+        raise ValueError("ids must be an int32 vector")
+    M = ids.shape[0]
+    size = int(lib().qlin_adapters_plan_size(M, adapters))
+    if out is None:
+        out = AdapterPlan(torch.empty(max(size, 16), dtype=torch.uint8, device=ids.device), M, adapters)
+    elif (out.tokens, out.adapters) != (M, adapters) or out.buffer.device != ids.device:
+        raise ValueError("out is a plan of other sizes or on another device")
+    with torch.cuda.device(ids.device):
+        _check(lib().qlin_adapters_plan(_ptr(ids), M, adapters, _ptr(out.buffer), out.buffer.numel(),
+                                        _stream(ids.device)), "qlin_adapters_plan")
+    return out
+
+
+def adapters_workspace_size(M: int, N: int, K: int, adapters: int, rank: int, backward: bool = False) -> int:
+    return int(lib().qlin_adapters_workspace_size(M, N, K, adapters, rank, int(backward)))
+
+
+def _adapter_sizes(t, a, b, plan):
+    if t.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("activations must be matrices and adapter factors [adapters, ., .]")
+    L, R, K = a.shape
+    if (plan.tokens, plan.adapters) != (t.shape[0], L) or plan.buffer.device != t.device:
+        raise ValueError(f"the plan is of {plan.tokens} tokens and {plan.adapters} adapters on {plan.buffer.device}")
+    return t.shape[0], b.shape[1], K, L, R
+
+
+def adapters_forward(x, a, b, scales, plan: AdapterPlan, base=None, out=None, u=None, workspace=None):
+    """out[m] = base[m] + scales[i] * b[i] @ (a[i] @ x[m]), i the adapter of token m (base[m] without one).
+
+    x [M, K], a [L, R, K], b [L, N, R], base [M, N] or None (zeros), all of one dtype; scales fp32 [L].
+    out may be base.  u: fp32 [M, R] to fill with a[i] @ x[m], for adapters_backward."""
+    M, N, K, L, R = _adapter_sizes(x, a, b, plan)
+    if out is None:
+        out = torch.empty((M, N), dtype=x.dtype, device=x.device)
+    _expect(x.device, x.dtype, x=(x, (M, K)), a=(a, (L, R, K)), b=(b, (L, N, R)), scales=(scales, (L,), torch.float32),
+            base=(base, (M, N)), out=(out, (M, N)), u=(u, (M, R), torch.float32))
+    ws = _workspace(workspace, adapters_workspace_size(M, N, K, L, R), x.device)
+    with torch.cuda.device(x.device):
+        _check(lib().qlin_adapters_forward(_ptr(x), _dt(x), M, K, _ptr(a), _ptr(b), _ptr(scales), L, R, N,
+                                           _ptr(plan.buffer), plan.buffer.numel(), _ptr(base), _ptr(out), _ptr(u),
+                                           _ptr(ws), ws.numel(), _stream(x.device)), "qlin_adapters_forward")
+    return out
+
+
+def adapters_backward(dy, a, b, scales, plan: AdapterPlan, u, x=None, checkpoint=None, dx_base=None, dx=None,
+                      want_dx: bool = True, workspace=None):
+    """(dx, da, db) of adapters_forward for the output gradient dy [M, N].
+
+    u: what the forward call filled.  The layer's input: x [M, K], or checkpoint = (q, scale, group_size) with
+    q, scale = quantize_int8_groups(x, group_size).  dx = dx_base (None: zeros) + the adapters' part, into dx if
+    given (it may be dx_base); want_dx=False: dx is None.  Adapters without tokens get zero gradients."""
+    M, N, K, L, R = _adapter_sizes(dy, a, b, plan)
+    q, q_scale, g = checkpoint if checkpoint is not None else (None, None, 0)
+    if (x is None) == (q is None):
+        raise ValueError("one of x and checkpoint")
+    if dx is None and want_dx:
+        dx = torch.empty((M, K), dtype=dy.dtype, device=dy.device)
+    if not want_dx and (dx is not None or dx_base is not None):
+        raise ValueError("dx and dx_base belong to want_dx=True")
+    _expect(dy.device, dy.dtype, dy=(dy, (M, N)), a=(a, (L, R, K)), b=(b, (L, N, R)),
+            scales=(scales, (L,), torch.float32), u=(u, (M, R), torch.float32), x=(x, (M, K)),
+            q=(q, (M, K), torch.int8), q_scale=(q_scale, (K // g if g > 0 else 0, M), torch.float32),
+            dx_base=(dx_base, (M, K)), dx=(dx, (M, K)))
+    da, db = torch.empty_like(a), torch.empty_like(b)
+    ws = _workspace(workspace, adapters_workspace_size(M, N, K, L, R, True), dy.device)
+    with torch.cuda.device(dy.device):
+        _check(lib().qlin_adapters_backward(_ptr(dy), _dt(dy), M, N, _ptr(a), _ptr(b), _ptr(scales), L, R, K,
+                                            _ptr(plan.buffer), plan.buffer.numel(), _ptr(u), _ptr(x), _ptr(q),
+                                            _ptr(q_scale), g, _ptr(dx_base), _ptr(dx), _ptr(da), _ptr(db), _ptr(ws),
+                                            ws.numel(), _stream(dy.device)), "qlin_adapters_backward")
+    return dx, da, db
+
+
+def dequantize_int8_groups(q, scale, group_size: int, out_dtype=torch.bfloat16, out=None):
+    """Restores quantize_int8_groups: q [N, K] * scale [K/group_size, N], rounded to out_dtype."""
+    if q.dim() != 2:
+        raise ValueError("q must be a matrix")
+    N, K = q.shape
+    if out is None:
+        out = torch.empty((N, K), dtype=out_dtype, device=q.device)
+    _expect(q.device, out_dtype, q=(q, (N, K), torch.int8), out=(out, (N, K)),
+            scale=(scale, (K // group_size if group_size > 0 else 0, N), torch.float32))
+    with torch.cuda.device(q.device):
+        _check(lib().qlin_dequantize_int8_groups(_ptr(q), _ptr(scale), N, K, group_size, _ptr(out), _dt(out),
+                                                 _stream(q.device)), "qlin_dequantize_int8_groups")
+    return out
+
+
+def pergroup_wgrad(dy, q, scale, group_size: int, bias: bool = True, dw=None):
+    """(dw, db) of a linear layer from dy [M, N] and its input's 8-bit checkpoint (q, scale); db None without bias."""
+    if dy.dim() != 2 or q.dim() != 2:
+        raise ValueError("dy and q must be matrices")
+    M, N = dy.shape
+    K = q.shape[1]
+    if dw is None:
+        dw = torch.empty((N, K), dtype=dy.dtype, device=dy.device)
+    _expect(dy.device, dy.dtype, dy=(dy, (M, N)), q=(q, (M, K), torch.int8), dw=(dw, (N, K)),
+            scale=(scale, (K // group_size if group_size > 0 else 0, M), torch.float32))
+    db = torch.empty((N,), dtype=dy.dtype, device=dy.device) if bias else None
+    with torch.cuda.device(dy.device):
+        _check(lib().pergroup_wgrad(_ptr(dy), _dt(dy), M, N, _ptr(q), _ptr(scale), K, group_size, _ptr(dw), _ptr(db),
+                                    _stream(dy.device)), "pergroup_wgrad")
+    return dw, db

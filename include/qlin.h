@@ -338,6 +338,96 @@ qlin_status w8a8_linear_noalloc(const void* x, qlin_dtype x_dt, int64_t M, int64
                                 const float* scale_w, int64_t N, const void* bias, void* y, void* stream);
 
 /*
+ * Low-rank adapters of many requests beside a shared projection.  Token m of a
+ * batch belongs to a request with adapter i = ids[m] (a pair of factors A_i,
+ * B_i and a scale s_i), or to none (ids[m] outside 0 .. L-1):
+ *   out[m] = base[m] + s_i * B_i (A_i x[m])       (base[m] without an adapter)
+ * base is what any layer call above gave for x.
+ *
+ * qlin_adapters_plan orders the tokens of a batch by adapter.  A plan depends
+ * on ids alone: one serves every layer of a model, forward and backward, until
+ * the batch changes.  ids: int32 [M] on the device, in any order; plan:
+ * qlin_adapters_plan_size(M, L) bytes, 16-byte aligned, written whole.
+ * 1 <= M <= 2^20, 1 <= L <= 1024 (QLIN_ERR_UNSUPPORTED above).
+ * qlin_adapters_plan_size gives 0 for sizes outside these.
+ */
+size_t qlin_adapters_plan_size(int64_t M, int64_t L);
+qlin_status qlin_adapters_plan(const int32_t* ids, int64_t M, int64_t L, void* plan, size_t plan_bytes, void* stream);
+
+/*
+ * Bytes of device workspace a forward (backward = 0) or backward (1) adapter
+ * call needs (0 = none, or sizes the calls refuse).
+ */
+size_t qlin_adapters_workspace_size(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R, int backward);
+
+/*
+ * Adapters, forward.  x: [M, K]; a: [L, R, K] and b: [L, N, R], the factors of
+ * every adapter (a rank below R: zero rows of a_i, zero columns of b_i);
+ * scales: fp32 [L]; base: [M, N] or NULL (zeros); out: [M, N], may be base
+ * itself (no other overlap); all of dtype dt.  plan: of the same M and L.
+ * u: fp32 [M, R] or NULL: gets A_i x[m], zero without an adapter -- what the
+ * backward pass needs.  1 <= R <= 128; K, N < 2^21 (QLIN_ERR_UNSUPPORTED
+ * otherwise).  Accumulation in fp32, u split into two 16-bit halves (a
+ * relative error of 2^-16 at most) for the second product, one rounding of
+ * the sum to dt.  fp32, and R, K or N that is not a multiple of 8, or tensors
+ * that are not 16-byte aligned, take slower kernels.  workspace:
+ * qlin_adapters_workspace_size(M, N, K, L, R, 0) bytes, 256-byte aligned.
+ * Results do not depend on the order of other requests' tokens in the batch
+ * beyond rounding, and are the same from run to run.
+ */
+qlin_status qlin_adapters_forward(const void* x, qlin_dtype dt, int64_t M, int64_t K, const void* a, const void* b,
+                                  const float* scales, int64_t L, int64_t R, int64_t N, const void* plan,
+                                  size_t plan_bytes, const void* base, void* out, float* u, void* workspace,
+                                  size_t ws_bytes, void* stream);
+
+/*
+ * Adapters, backward.  With v[m] = s_i * B_i^T dy[m]:
+ *   dx[m] = dx_base[m] + A_i^T v[m]         (dx_base[m] without an adapter)
+ *   da_i  = sum over i's tokens of v[m] x[m]^T           [R, K]
+ *   db_i  = s_i * sum over i's tokens of dy[m] u[m]^T    [N, R]
+ * dy: [M, N]; a, b, scales, plan: as forward; u: fp32 [M, R] of the forward
+ * call; the layer's input either as x: [M, K] (q = NULL), or as its 8-bit
+ * checkpoint (x = NULL): q: int8 [M, K] and q_scale: fp32 [K/group_size, M] of
+ * qlin_quantize_int8_groups(x).  dx_base: [M, K], the gradient that the shared
+ * projection passes on, or NULL (zeros); dx: [M, K], may be dx_base itself, or
+ * NULL (not wanted).  da: [L, R, K], db: [L, N, R], written whole: zeros for
+ * adapters without tokens.  All of dtype dt.  Sizes as forward; with a
+ * checkpoint group_size in {64, 128, 256} and K % group_size == 0.  Sums over
+ * tokens have a fixed order.  workspace:
+ * qlin_adapters_workspace_size(M, N, K, L, R, 1) bytes, 256-byte aligned.
+ */
+qlin_status qlin_adapters_backward(const void* dy, qlin_dtype dt, int64_t M, int64_t N, const void* a, const void* b,
+                                   const float* scales, int64_t L, int64_t R, int64_t K, const void* plan,
+                                   size_t plan_bytes, const float* u, const void* x, const int8_t* q,
+                                   const float* q_scale, int group_size, const void* dx_base, void* dx, void* da,
+                                   void* db, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Activations kept in 8 bits for the backward pass.  The checkpoint of a
+ * layer's input x [M tokens, K] is qlin_quantize_int8_groups(x): q int8 [M, K]
+ * and scale fp32 [K/group_size, M].  qlin_dequantize_int8_groups restores it
+ * (or a per-group INT8 weight): out[n, k] = q[n, k] * scale[k/group_size, n],
+ * one fp32 product rounded to out_dt.  q: int8 [N, K], out: [N, K], both
+ * 16-byte aligned.  group_size in {64, 128, 256}; K % group_size == 0.
+ */
+qlin_status qlin_dequantize_int8_groups(const int8_t* q, const float* scale, int64_t N, int64_t K, int group_size,
+                                        void* out, qlin_dtype out_dt, void* stream);
+
+/*
+ * Weight gradient of a linear layer whose input was kept in 8 bits:
+ *   dw[n, k] = sum_m dy[m, n] * q[m, k] * scale[k/group_size, m]
+ *   db[n]    = sum_m dy[m, n]                    (db may be NULL)
+ * dy: [M, N] of dt, bf16 or fp16 (QLIN_ERR_UNSUPPORTED for fp32); q: int8
+ * [M, K], scale: fp32 [K/group_size, M]; dw: [N, K], db: [N] of dt, written
+ * whole.  Each restored input is rounded once to dt as the tensor cores'
+ * operand; sums in fp32 in a fixed order, one rounding to dt.  N % 8 == 0,
+ * dy, q and dw 16-byte aligned (QLIN_ERR_MISALIGNED); group_size in
+ * {64, 128, 256}, K % group_size == 0, K < 2^21.
+ */
+qlin_status pergroup_wgrad(const void* dy, qlin_dtype dt, int64_t M, int64_t N, const int8_t* q, const float* scale,
+                           int64_t K, int group_size, void* dw, void* db, void* stream);
+
+/*
  * Synchronises `stream`, then reports (and clears) the library's device
  * status word: QLIN_ERR_TIMEOUT if a bounded on-device wait in any kernel
  * gave up since the last call, QLIN_ERR_CUDA if the stream holds an error,
