@@ -6,7 +6,7 @@
 //
 //   restore   x^ in the type asked for
 //   wgrad     dW[n][k] = sum_m dy[m][n] x^[m][k]      db[n] = sum_m dy[m][n]
-#include "simt_tile.cuh"
+#include "qlin_common.cuh"
 
 namespace qlin {
 
@@ -52,53 +52,377 @@ __global__ void __launch_bounds__(256) dequantize_int8_groups_kernel(const int8_
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) wgrad_kernel(const T* __restrict__ dy, const int8_t* __restrict__ q,
-                                                         const float* __restrict__ scale, int64_t M, int64_t N,
-                                                         int64_t K, int g_shift, T* __restrict__ dw)
+// ------------------------------------------------------------------------------------ wgrad
+//
+// A persistent, warp-specialised tcgen05 GEMM over tiles of 128 MT outputs n by 256 inputs k.  The
+// contraction runs over tokens, the slow dimension of both operands in memory, so both are read
+// MN-major (a shared-memory row holds one token's 64 outputs or inputs, 128 bytes, 128-byte
+// swizzle) and nothing is transposed:
+//   warp 0        TMA producer: dy boxes {64 outputs, 64 tokens}, the A operand as it is, and code
+//                 boxes {128 bytes, 64 tokens}
+//   warp 1        512 columns of tensor memory; one thread issues M = 128, N = 256, K = 16 MMAs, MT
+//                 of them on each decoded B step
+//   warps 2..9    decode: 16 codes (one 16-byte load) -> s q in fp32, rounded once to the operand
+//                 type, two 16-byte swizzled stores.  Eight lanes of a load or store phase cover
+//                 rows r and r + 4 of one 64-input atom, which meet no bank twice
+//   warps 10..    epilogue: 32 rows n each, 16-byte stores of dW
+// MT = 2 (two accumulators on one decoded step) halves the decode work and the code bytes per
+// product; MT = 1 keeps two accumulators in turn, so that a tile is written while the next one is
+// multiplied.
+constexpr int kXWarps = 8;
+constexpr int kKT = 256;      // inputs k of a tile
+constexpr int kStageM = 64;   // tokens of a stage
+
+__host__ __device__ constexpr int cmin(int a, int b) { return a < b ? a : b; }
+
+template <int MT>
+struct WgCfg {
+    static constexpr int TN = 128 * MT;
+    static constexpr int A_BYTES = TN * kStageM * 2;
+    static constexpr int RAW_BYTES = kKT * kStageM;
+    static constexpr int B_BYTES = kKT * kStageM * 2;
+    static constexpr int SLOT = A_BYTES + RAW_BYTES;
+    static constexpr int NB = 2;
+    static constexpr int NS = cmin(4, (225 * 1024 - NB * B_BYTES) / SLOT);
+    static constexpr int BUFS = MT == 2 ? 1 : 2;
+    static constexpr int EW = 4 * MT;
+    static constexpr int THREADS = (2 + kXWarps + EW) * 32;
+    struct Bars {
+        uint64_t full[NS], empty[NS], bfull[NB], bempty[NB], acc_full[2], acc_empty[2], mma_done;
+        uint32_t tmem;
+        int abort_flag;
+    };
+    static constexpr int SMEM = NS * SLOT + NB * B_BYTES + (int)sizeof(Bars) + 1024;
+    static_assert(SMEM <= 227 * 1024 && NS >= 3, "shared memory");
+};
+
+struct WgParams {
+    CUtensorMap tm_dy;  // [M][N] 16-bit, box {64, 64}, 128-byte swizzle
+    CUtensorMap tm_q;   // [M][K] bytes, box {128, 64}, 128-byte swizzle
+    const float* scale; // [K/g][M]
+    void* dw;           // [N][K]
+    int64_t M, N, K;
+    int g_shift;
+    int tiles_n, tiles_k;
+    int f16;
+    unsigned* status;
+};
+
+QLIN_DEV bool aborted(int* flag) { return *reinterpret_cast<volatile int*>(flag) != 0; }
+
+QLIN_DEV void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
-    const int64_t n0 = (int64_t)blockIdx.x * kB, k0 = (int64_t)blockIdx.y * kB;
-    float o[4][4];
-    tile_product<false, false>(
-        0, M, [&](int i, int64_t m) { return n0 + i < N ? to_float(dy[m * N + n0 + i]) : 0.f; },
-        [&](int j, int64_t m) { return (float)q[m * K + k0 + j] * scale[((k0 + j) >> g_shift) * M + m]; }, o);
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+QLIN_DEV uint4 ld_shared_v4(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// Code i of u (codes ^ 0x80, so 0 .. 255) as an exact fp32: the byte in the mantissa of 2^23.
+QLIN_DEV float code_f32(uint32_t u, int i)
+{
+    return __uint_as_float(prmt(u, 0x4B000000u, 0x7650u + (uint32_t)i)) - 8388736.f;
+}
+
+// Groups of 8 tiles along n walk the k tiles together: their dy columns and the codes stay in L2.
+QLIN_DEV void wg_tile(int t, int tiles_n, int tiles_k, int& nt, int& kt)
+{
+    constexpr int G = 8;
+    const int grp = t / (G * tiles_k), first = grp * G, gn = min(G, tiles_n - first), r = t - grp * G * tiles_k;
+    nt = first + r % gn;
+    kt = r / gn;
+}
+
+template <int MT>
+__global__ void __launch_bounds__(WgCfg<MT>::THREADS, 1) wgrad_tc_kernel(const __grid_constant__ WgParams p)
+{
+    using C = WgCfg<MT>;
+    using Bars = typename C::Bars;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Bars& bars = *reinterpret_cast<Bars*>(smem + C::NS * C::SLOT + C::NB * C::B_BYTES);
+    auto A = [&](int s) { return smem + s * C::SLOT; };
+    auto RAW = [&](int s) { return smem + s * C::SLOT + C::A_BYTES; };
+    auto BT = [&](int b) { return smem + C::NS * C::SLOT + b * C::B_BYTES; };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nm = (int)((p.M + kStageM - 1) / kStageM);
+    const int tiles = p.tiles_n * p.tiles_k;
+    const int my_tiles = tiles > (int)blockIdx.x ? (tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::NS; ++s) {
+            mbar_init(&bars.full[s], 1);
+            mbar_init(&bars.empty[s], 1);
+        }
+        for (int b = 0; b < C::NB; ++b) {
+            mbar_init(&bars.bfull[b], kXWarps);
+            mbar_init(&bars.bempty[b], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&bars.acc_full[b], 1);
+            mbar_init(&bars.acc_empty[b], C::EW);
+        }
+        mbar_init(&bars.mma_done, 1);
+        bars.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1)
+        tmem_alloc(&bars.tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars.tmem;
+    pdl_wait_prior_grids();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;
+            bool ok = true;
+            for (int ti = 0; ti < my_tiles && ok; ++ti) {
+                int nt, kt;
+                wg_tile((int)blockIdx.x + ti * (int)gridDim.x, p.tiles_n, p.tiles_k, nt, kt);
+                for (int mb = 0; mb < nm; ++mb, ++it) {
+                    const int slot = it % C::NS;
+                    if ((it >= C::NS &&
+                         !mbar_wait_bounded(&bars.empty[slot], ((it / C::NS) & 1) ^ 1, p.status)) ||
+                        aborted(&bars.abort_flag)) {
+                        bars.abort_flag = 1;
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&bars.full[slot], C::SLOT);
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+                    for (int h = 0; h < 2; ++h)
+                        tma_load_2d(RAW(slot) + h * 128 * kStageM, &p.tm_q, kt * kKT + h * 128, mb * kStageM,
+                                    &bars.full[slot]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-            if (n0 + 4 * ty + r < N)
-                dw[(n0 + 4 * ty + r) * K + k0 + 4 * tx + c] = from_float<T>(o[r][c]);
+                    for (int a = 0; a < 2 * MT; ++a)
+                        tma_load_2d(A(slot) + a * 128 * kStageM, &p.tm_dy, nt * C::TN + a * 64, mb * kStageM,
+                                    &bars.full[slot]);
+                }
+            }
+            for (int j = it - C::NS < 0 ? 0 : it - C::NS; j < it; ++j)  // no copy may land after the exit
+                mbar_wait_bounded(&bars.full[j % C::NS], (j / C::NS) & 1, p.status);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // D f32; A, B of one 16-bit type (bf16 = 1), both MN-major; N = 256, M = 128
+            const uint32_t ty = p.f16 ? 0u : (1u << 7) | (1u << 10);
+            const uint32_t idesc =
+                (1u << 4) | ty | (1u << 15) | (1u << 16) | ((uint32_t)(kKT >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+            constexpr uint32_t ATOM = 128 * kStageM;
+            int it = 0;
+            bool ok = true;
+            for (int ti = 0; ti < my_tiles && ok; ++ti) {
+                const int buf = ti % C::BUFS;
+                ok = mbar_wait_bounded(&bars.acc_empty[buf], ((ti / C::BUFS) & 1) ^ 1, p.status);
+                tc_fence_after();
+                const uint32_t acc = tmem + (uint32_t)(buf * 256);
+                for (int mb = 0; mb < nm && ok; ++mb, ++it) {
+                    const int slot = it % C::NS, b = it % C::NB;
+                    ok = mbar_wait_bounded(&bars.full[slot], (it / C::NS) & 1, p.status) &&
+                         mbar_wait_bounded(&bars.bfull[b], (it / C::NB) & 1, p.status);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    const uint32_t a0 = smem_u32(A(slot)), b0 = smem_u32(BT(b));
+#pragma unroll
+                    for (int kk = 0; kk < kStageM / 16; ++kk) {
+                        const uint64_t bd = umma_desc_sw128_mn(b0 + kk * 2048, ATOM);
+#pragma unroll
+                        for (int m = 0; m < MT; ++m)
+                            tc_mma<false>(acc + (uint32_t)(m * 256),
+                                          umma_desc_sw128_mn(a0 + m * 2 * ATOM + kk * 2048, ATOM), bd, idesc,
+                                          (mb | kk) != 0 ? 1u : 0u);
+                    }
+                    tc_commit(&bars.empty[slot]);
+                    tc_commit(&bars.bempty[b]);
+                }
+                tc_commit(&bars.acc_full[buf]);
+            }
+            if (!ok)
+                bars.abort_flag = 1;
+            tc_commit(&bars.mma_done);  // every MMA issued has completed before TMEM is released
+            mbar_wait_bounded(&bars.mma_done, 0, p.status);
+        }
+        __syncwarp();
+    } else if (warp < 2 + kXWarps) {
+        const int w = warp - 2, atom = w & 3;
+        const int row0 = (w >> 2) * 32 + (lane >> 3) + ((lane >> 2) & 1) * 4;  // + 8 j, j = 0 .. 3
+        const int unit = (atom & 1) * 4 + (lane & 3), bunit = 2 * (lane & 3), swap = (lane >> 2) & 1;
+        int it = 0;
+        bool ok = true;
+        for (int ti = 0; ti < my_tiles && ok; ++ti) {
+            int nt, kt;
+            wg_tile((int)blockIdx.x + ti * (int)gridDim.x, p.tiles_n, p.tiles_k, nt, kt);
+            const int64_t k = (int64_t)kt * kKT + atom * 64;
+            const float* sc = k < p.K ? p.scale + (k >> p.g_shift) * p.M : nullptr;
+            float s[4], next[4];
+            auto load_scales = [&](int mb, float (&d)[4]) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int64_t m = (int64_t)mb * kStageM + row0 + 8 * j;
+                    d[j] = sc && m < p.M ? __ldg(sc + m) : 0.f;
+                }
+            };
+            load_scales(0, next);
+            for (int mb = 0; mb < nm; ++mb, ++it) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    s[j] = next[j];
+                if (mb + 1 < nm)
+                    load_scales(mb + 1, next);
+                const int slot = it % C::NS, b = it % C::NB;
+                if (!mbar_wait_bounded(&bars.full[slot], (it / C::NS) & 1, p.status) ||
+                    !mbar_wait_bounded(&bars.bempty[b], ((it / C::NB) & 1) ^ 1, p.status) ||
+                    aborted(&bars.abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t raw = smem_u32(RAW(slot)) + (atom >> 1) * 128 * kStageM;
+                const uint32_t dst = smem_u32(BT(b)) + atom * 128 * kStageM;
+                uint4 v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[j] = ld_shared_v4(raw + swz128(row0 + 8 * j, unit));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int row = row0 + 8 * j;
+                    const uint32_t c[4] = {v[j].x ^ 0x80808080u, v[j].y ^ 0x80808080u, v[j].z ^ 0x80808080u,
+                                           v[j].w ^ 0x80808080u};
+                    uint32_t h[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        h[2 * e] = pack_h16x2(code_f32(c[e], 0) * s[j], code_f32(c[e], 1) * s[j], p.f16);
+                        h[2 * e + 1] = pack_h16x2(code_f32(c[e], 2) * s[j], code_f32(c[e], 3) * s[j], p.f16);
+                    }
+                    // rows r + 4 of a phase store their second half first
+                    const uint32_t first = dst + swz128(row, bunit + swap), second = dst + swz128(row, bunit + 1 - swap);
+                    if (swap) {
+                        st_shared_v4(first, h[4], h[5], h[6], h[7]);
+                        st_shared_v4(second, h[0], h[1], h[2], h[3]);
+                    } else {
+                        st_shared_v4(first, h[0], h[1], h[2], h[3]);
+                        st_shared_v4(second, h[4], h[5], h[6], h[7]);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&bars.bfull[b]);
+            }
+        }
+        if (!ok)
+            bars.abort_flag = 1;
+    } else {
+        const int q = warp & 3, sub = (warp - 2 - kXWarps) >> 2;
+        for (int ti = 0; ti < my_tiles; ++ti) {
+            const int buf = ti % C::BUFS;
+            if (!mbar_wait_bounded(&bars.acc_full[buf], (ti / C::BUFS) & 1, p.status) || aborted(&bars.abort_flag)) {
+                bars.abort_flag = 1;
+                break;
+            }
+            tc_fence_after();
+            int nt, kt;
+            wg_tile((int)blockIdx.x + ti * (int)gridDim.x, p.tiles_n, p.tiles_k, nt, kt);
+            const int64_t n = (int64_t)nt * C::TN + sub * 128 + 32 * q + lane;
+            const uint32_t acc = tmem + (uint32_t)((buf + sub) * 256) + ((uint32_t)(32 * q) << 16);
+            unsigned short* o = static_cast<unsigned short*>(p.dw) + n * p.K + (int64_t)kt * kKT;
+            const int cols = (int)(p.K - (int64_t)kt * kKT < kKT ? p.K - (int64_t)kt * kKT : kKT);  // K % 64 == 0
+#pragma unroll 1
+            for (int c = 0; c < cols; c += 32) {
+                uint32_t r[2][16];
+                tmem_ld16_nowait(acc + (uint32_t)c, r[0]);
+                tmem_ld16_nowait(acc + (uint32_t)c + 16u, r[1]);
+                tmem_wait_ld();
+                if (n < p.N) {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = pack_h16x2(__uint_as_float(r[h >> 1][(h & 1) * 8 + 2 * e]),
+                                              __uint_as_float(r[h >> 1][(h & 1) * 8 + 2 * e + 1]), p.f16);
+                        *reinterpret_cast<uint4*>(o + c + 8 * h) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&bars.acc_empty[buf]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1)
+        tmem_dealloc(tmem, 512);
 }
 
 template <typename T>
 __global__ void __launch_bounds__(256) column_sum_kernel(const T* __restrict__ dy, int64_t M, int64_t N,
                                                          T* __restrict__ db)
 {
-    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (n >= N)
-        return;
-    float sum = 0.f;
-    for (int64_t m0 = 0; m0 < M; m0 += kChunk) {
-        float part = 0.f;
-        for (int64_t m = m0; m < (m0 + kChunk < M ? m0 + kChunk : M); ++m)
-            part += to_float(dy[m * N + n]);
-        sum += part;
+    // 64 columns a CTA: 8 threads of 8 columns along a row, 32 rows at a time
+    __shared__ float part[32][64];
+    const int64_t n = (int64_t)blockIdx.x * 64 + (threadIdx.x & 7) * 8;
+    const int r = threadIdx.x >> 3;
+    float sum[8] = {};
+    if (n < N) {
+#pragma unroll 8
+        for (int64_t m = r; m < M; m += 32) {
+            const uint4 v = ldg_stream_v4(dy + m * N + n);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sum[2 * e] += h16_to_float(w[e], !__is_same(T, __nv_bfloat16));
+                sum[2 * e + 1] += h16_to_float(w[e] >> 16, !__is_same(T, __nv_bfloat16));
+            }
+        }
     }
-    db[n] = from_float<T>(sum);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        part[r][(threadIdx.x & 7) * 8 + e] = sum[e];
+    __syncthreads();
+    if (threadIdx.x < 64 && (int64_t)blockIdx.x * 64 + threadIdx.x < N) {
+        float t = 0.f;
+        for (int i = 0; i < 32; ++i)
+            t += part[i][threadIdx.x];
+        db[(int64_t)blockIdx.x * 64 + threadIdx.x] = from_float<T>(t);
+    }
 }
 
 int log2_of(int g) { return g == 64 ? 6 : g == 128 ? 7 : 8; }
 
-template <typename T>
-cudaError_t wgrad_t(const T* dy, int64_t M, int64_t N, const int8_t* q, const float* scale, int64_t K, int g, T* dw,
-                    T* db, cudaStream_t st)
+template <int MT>
+cudaError_t launch_wgrad(WgParams& p, cudaStream_t st, const DeviceInfo& dev)
 {
-    wgrad_kernel<T><<<dim3((unsigned)((N + kB - 1) / kB), (unsigned)(K / kB)), kThreads, 0, st>>>(
-        dy, q, scale, M, N, K, log2_of(g), dw);
-    if (db)
-        column_sum_kernel<T><<<(unsigned)((N + 255) / 256), 256, 0, st>>>(dy, M, N, db);
-    return cudaGetLastError();
+    using C = WgCfg<MT>;
+    auto kern = wgrad_tc_kernel<MT>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess)
+        return e;
+    p.tiles_n = (int)((p.N + C::TN - 1) / C::TN);
+    p.tiles_k = (int)((p.K + kKT - 1) / kKT);
+    const int64_t tiles = (int64_t)p.tiles_n * p.tiles_k;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles < dev.sm_count ? tiles : dev.sm_count));
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 }  // namespace
@@ -120,13 +444,33 @@ cudaError_t launch_dequantize_int8_groups(const int8_t* q, const float* scale, i
 
 cudaError_t launch_pergroup_wgrad(const void* dy, qlin_dtype dt, int64_t M, int64_t N, const int8_t* q,
                                   const float* scale, int64_t K, int g, void* dw, void* db, cudaStream_t st,
-                                  const DeviceInfo&)
+                                  const DeviceInfo& dev)
 {
+    WgParams p;
+    p.scale = scale;
+    p.dw = dw;
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.g_shift = log2_of(g);
+    p.f16 = dt == QLIN_F16;
+    p.status = dev.status;
+    if (!encode_tmap_2d(&p.tm_dy, p.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy,
+                        (uint64_t)N, (uint64_t)M, (uint64_t)N * 2, 64, kStageM) ||
+        !encode_tmap_2d(&p.tm_q, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, (uint64_t)K, (uint64_t)M, (uint64_t)K, 128,
+                        kStageM))
+        return cudaErrorInvalidValue;
+    const bool two = N > 128 && M > 512;
+    const cudaError_t e = two ? launch_wgrad<2>(p, st, dev) : launch_wgrad<1>(p, st, dev);
+    if (e != cudaSuccess || !db)
+        return e;
+    const unsigned blocks = (unsigned)((N + 63) / 64);
     if (dt == QLIN_BF16)
-        return wgrad_t(static_cast<const __nv_bfloat16*>(dy), M, N, q, scale, K, g, static_cast<__nv_bfloat16*>(dw),
-                       static_cast<__nv_bfloat16*>(db), st);
-    return wgrad_t(static_cast<const __half*>(dy), M, N, q, scale, K, g, static_cast<__half*>(dw),
-                   static_cast<__half*>(db), st);
+        column_sum_kernel<<<blocks, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(dy), M, N,
+                                                  static_cast<__nv_bfloat16*>(db));
+    else
+        column_sum_kernel<<<blocks, 256, 0, st>>>(static_cast<const __half*>(dy), M, N, static_cast<__half*>(db));
+    return cudaGetLastError();
 }
 
 }  // namespace qlin
