@@ -91,4 +91,28 @@ size_t adapters_simt_workspace(int64_t M, int64_t N, int64_t K, int64_t R);
 cudaError_t launch_adapters_forward_simt(const AdapterFwdArgs& a, cudaStream_t st);
 cudaError_t launch_adapters_backward_simt(const AdapterBwdArgs& a, cudaStream_t st);
 
+
+// Tensor-core kernels (k_adapters_tc.cu): bf16 and fp16, R, K and N multiples of 8, every tensor
+// 16-byte aligned.
+bool adapters_tc_takes(const AdapterFwdArgs& a);
+bool adapters_tc_takes(const AdapterBwdArgs& a);
+size_t adapters_tc_workspace(int64_t M, int64_t L, int64_t R);
+cudaError_t launch_adapters_forward_tc(const AdapterFwdArgs& a, cudaStream_t st, const DeviceInfo& dev);
+cudaError_t launch_adapters_backward_tc(const AdapterBwdArgs& a, cudaStream_t st, const DeviceInfo& dev);
+
+// Host: a 3-D tensor map over dense [dim2][dim1][dim0] elements of elem_bytes, box {box0, box1, 1},
+// 128-byte swizzle, zero fill (qlin_abi.cu).
+bool encode_tmap_3d(CUtensorMap* tm, CUtensorMapDataType dt, const void* base, uint64_t dim0, uint64_t dim1,
+                    uint64_t dim2, uint64_t elem_bytes, uint32_t box0, uint32_t box1);
+
+// Loads the box at (c0, c1, c2) of a 3-D tensor map into this CTA's shared memory.
+QLIN_DEV void tma_load_3d(void* smem_dst, const CUtensorMap* tmap, int c0, int c1, int c2, uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+        : "memory");
+}
+
 }  // namespace qlin

@@ -589,7 +589,8 @@ size_t qlin_adapters_workspace_size(int64_t M, int64_t N, int64_t K, int64_t L, 
     if (check_plan(M, L) != QLIN_OK || N <= 0 || K <= 0 || R <= 0 || R > kMaxRank || N >= kMaxFeatures ||
         K >= kMaxFeatures)
         return 0;
-    return align256(adapters_simt_workspace(M, N, K, R));
+    const size_t simt = align256(adapters_simt_workspace(M, N, K, R)), tc = align256(adapters_tc_workspace(M, L, R));
+    return simt > tc ? simt : tc;
 }
 
 qlin_status qlin_adapters_forward(const void* x, qlin_dtype dt, int64_t M, int64_t K, const void* a, const void* b,
@@ -614,7 +615,8 @@ qlin_status qlin_adapters_forward(const void* x, qlin_dtype dt, int64_t M, int64
     if ((s = current_device(dev)) != QLIN_OK)
         return s;
     const AdapterFwdArgs f = {x, a, b, scales, base, out, u, dt, M, K, N, L, R, plan_view(plan, M, L), workspace};
-    return from_cuda(launch_adapters_forward_simt(f, static_cast<cudaStream_t>(stream)));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return from_cuda(adapters_tc_takes(f) ? launch_adapters_forward_tc(f, st, dev) : launch_adapters_forward_simt(f, st));
 }
 
 qlin_status qlin_adapters_backward(const void* dy, qlin_dtype dt, int64_t M, int64_t N, const void* a, const void* b,
@@ -646,7 +648,9 @@ qlin_status qlin_adapters_backward(const void* dy, qlin_dtype dt, int64_t M, int
     const AdapterBwdArgs g = {dy, a,  b,  scales, u,  x, q, q_scale, group_size, dx_base,
                               dx, da, db, dt,     M,  K, N, L,       R,          plan_view(plan, M, L),
                               workspace};
-    return from_cuda(launch_adapters_backward_simt(g, static_cast<cudaStream_t>(stream)));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return from_cuda(adapters_tc_takes(g) ? launch_adapters_backward_tc(g, st, dev)
+                                          : launch_adapters_backward_simt(g, st));
 }
 
 qlin_status qlin_dequantize_int8_groups(const int8_t* q, const float* scale, int64_t N, int64_t K, int group_size,
@@ -731,8 +735,9 @@ qlin_status qlin_get_device_status(void* stream)
 
 namespace qlin {
 
-bool encode_tmap_2d(CUtensorMap* tm, CUtensorMapDataType dt, const void* base, uint64_t dim0, uint64_t dim1,
-                    uint64_t pitch_bytes, uint32_t box0, uint32_t box1, CUtensorMapSwizzle swizzle)
+namespace {
+
+PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder()
 {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     static std::once_flag once;
@@ -745,6 +750,15 @@ bool encode_tmap_2d(CUtensorMap* tm, CUtensorMapDataType dt, const void* base, u
         else
             cudaGetLastError();
     });
+    return fn;
+}
+
+}  // namespace
+
+bool encode_tmap_2d(CUtensorMap* tm, CUtensorMapDataType dt, const void* base, uint64_t dim0, uint64_t dim1,
+                    uint64_t pitch_bytes, uint32_t box0, uint32_t box1, CUtensorMapSwizzle swizzle)
+{
+    const PFN_cuTensorMapEncodeTiled_v12000 fn = tmap_encoder();
     if (!fn)
         return false;
     cuuint64_t dims[2] = {dim0, dim1};
@@ -753,6 +767,21 @@ bool encode_tmap_2d(CUtensorMap* tm, CUtensorMapDataType dt, const void* base, u
     cuuint32_t estr[2] = {1, 1};
     return fn(tm, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_tmap_3d(CUtensorMap* tm, CUtensorMapDataType dt, const void* base, uint64_t dim0, uint64_t dim1,
+                    uint64_t dim2, uint64_t elem_bytes, uint32_t box0, uint32_t box1)
+{
+    const PFN_cuTensorMapEncodeTiled_v12000 fn = tmap_encoder();
+    if (!fn)
+        return false;
+    cuuint64_t dims[3] = {dim0, dim1, dim2};
+    cuuint64_t strides[2] = {dim0 * elem_bytes, dim0 * dim1 * elem_bytes};
+    cuuint32_t box[3] = {box0, box1, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(tm, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace qlin
