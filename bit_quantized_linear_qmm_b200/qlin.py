@@ -317,27 +317,43 @@ def quantize_weight_int8(w, clip_percentile=None):
     return q, s
 
 
-def _expect(device, dtype, **tensors):
-    """Each of name=(tensor or None, shape[, dtype]): a contiguous CUDA tensor on `device` of that shape and type."""
-    for name, (t, shape, *dt) in tensors.items():
-        if t is None:
-            continue
-        _cuda(t)
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-        if t.dtype != (dt[0] if dt else dtype):
-            raise TypeError(f"{name} has dtype {t.dtype}, not {dt[0] if dt else dtype}")
+def _misfit(name, t, shape, dtype, dev):
+    _cuda(t)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    raise TypeError(f"{name} has dtype {t.dtype}, not {dtype}")
 
 
-def _workspace(workspace, need: int, device):
+def _fit(name, t, shape, dtype, dev):
+    """Address of a contiguous CUDA tensor of that shape and type on device number dev (None: none); raises else."""
+    if t is None:
+        return None
+    if t.get_device() != dev or t.shape != shape or t.dtype != dtype or dev < 0 or not t.is_contiguous():
+        _misfit(name, t, shape, dtype, dev)
+    return t.data_ptr()
+
+
+def _space(workspace, need: int, dev: int, like):
+    """(address, bytes) of the caller's workspace, or of one from torch's allocator; the tensor keeps it alive."""
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    _cuda(workspace)
-    if workspace.device != device:
-        raise ValueError(f"workspace is on {workspace.device}, not on {device}")
-    return workspace
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on cuda:{dev}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _run(name, dev: int, *args):
+    """Calls a library function on device dev and its current stream."""
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if status != QLIN_OK:
+        _check(status, name)
 
 
 class AdapterPlan(NamedTuple):
@@ -360,9 +376,7 @@ def adapters_plan(ids, adapters: int, out: AdapterPlan | None = None) -> Adapter
         out = AdapterPlan(torch.empty(max(size, 16), dtype=torch.uint8, device=ids.device), M, adapters)
     elif (out.tokens, out.adapters) != (M, adapters) or out.buffer.device != ids.device:
         raise ValueError("out is a plan of other sizes or on another device")
-    with torch.cuda.device(ids.device):
-        _check(lib().qlin_adapters_plan(_ptr(ids), M, adapters, _ptr(out.buffer), out.buffer.numel(),
-                                        _stream(ids.device)), "qlin_adapters_plan")
+    _run("qlin_adapters_plan", ids.get_device(), ids.data_ptr(), M, adapters, out.buffer.data_ptr(), out.buffer.numel())
     return out
 
 
@@ -374,9 +388,10 @@ def _adapter_sizes(t, a, b, plan):
     if t.dim() != 2 or a.dim() != 3 or b.dim() != 3:
         raise ValueError("activations must be matrices and adapter factors [adapters, ., .]")
     L, R, K = a.shape
-    if (plan.tokens, plan.adapters) != (t.shape[0], L) or plan.buffer.device != t.device:
+    M, dev = t.shape[0], t.get_device()
+    if plan.tokens != M or plan.adapters != L or plan.buffer.get_device() != dev:
         raise ValueError(f"the plan is of {plan.tokens} tokens and {plan.adapters} adapters on {plan.buffer.device}")
-    return t.shape[0], b.shape[1], K, L, R
+    return M, b.shape[1], K, L, R, dev
 
 
 def adapters_forward(x, a, b, scales, plan: AdapterPlan, base=None, out=None, u=None, workspace=None):
@@ -384,16 +399,15 @@ def adapters_forward(x, a, b, scales, plan: AdapterPlan, base=None, out=None, u=
 
     x [M, K], a [L, R, K], b [L, N, R], base [M, N] or None (zeros), all of one dtype; scales fp32 [L].
     out may be base.  u: fp32 [M, R] to fill with a[i] @ x[m], for adapters_backward."""
-    M, N, K, L, R = _adapter_sizes(x, a, b, plan)
+    M, N, K, L, R, dev = _adapter_sizes(x, a, b, plan)
+    dt = x.dtype
     if out is None:
-        out = torch.empty((M, N), dtype=x.dtype, device=x.device)
-    _expect(x.device, x.dtype, x=(x, (M, K)), a=(a, (L, R, K)), b=(b, (L, N, R)), scales=(scales, (L,), torch.float32),
-            base=(base, (M, N)), out=(out, (M, N)), u=(u, (M, R), torch.float32))
-    ws = _workspace(workspace, adapters_workspace_size(M, N, K, L, R), x.device)
-    with torch.cuda.device(x.device):
-        _check(lib().qlin_adapters_forward(_ptr(x), _dt(x), M, K, _ptr(a), _ptr(b), _ptr(scales), L, R, N,
-                                           _ptr(plan.buffer), plan.buffer.numel(), _ptr(base), _ptr(out), _ptr(u),
-                                           _ptr(ws), ws.numel(), _stream(x.device)), "qlin_adapters_forward")
+        out = torch.empty((M, N), dtype=dt, device=x.device)
+    ws, wp, wn = _space(workspace, lib().qlin_adapters_workspace_size(M, N, K, L, R, 0), dev, x)
+    _run("qlin_adapters_forward", dev, _fit("x", x, (M, K), dt, dev), _dt(x), M, K, _fit("a", a, (L, R, K), dt, dev),
+         _fit("b", b, (L, N, R), dt, dev), _fit("scales", scales, (L,), torch.float32, dev), L, R, N,
+         plan.buffer.data_ptr(), plan.buffer.numel(), _fit("base", base, (M, N), dt, dev),
+         _fit("out", out, (M, N), dt, dev), _fit("u", u, (M, R), torch.float32, dev), wp, wn)
     return out
 
 
@@ -404,25 +418,23 @@ def adapters_backward(dy, a, b, scales, plan: AdapterPlan, u, x=None, checkpoint
     u: what the forward call filled.  The layer's input: x [M, K], or checkpoint = (q, scale, group_size) with
     q, scale = quantize_int8_groups(x, group_size).  dx = dx_base (None: zeros) + the adapters' part, into dx if
     given (it may be dx_base); want_dx=False: dx is None.  Adapters without tokens get zero gradients."""
-    M, N, K, L, R = _adapter_sizes(dy, a, b, plan)
+    M, N, K, L, R, dev = _adapter_sizes(dy, a, b, plan)
+    dt, f32 = dy.dtype, torch.float32
     q, q_scale, g = checkpoint if checkpoint is not None else (None, None, 0)
-    if (x is None) == (q is None):
-        raise ValueError("one of x and checkpoint")
-    if dx is None and want_dx:
-        dx = torch.empty((M, K), dtype=dy.dtype, device=dy.device)
+    if (x is None) == (q is None) or u is None:
+        raise ValueError("u, and one of x and checkpoint")
     if not want_dx and (dx is not None or dx_base is not None):
         raise ValueError("dx and dx_base belong to want_dx=True")
-    _expect(dy.device, dy.dtype, dy=(dy, (M, N)), a=(a, (L, R, K)), b=(b, (L, N, R)),
-            scales=(scales, (L,), torch.float32), u=(u, (M, R), torch.float32), x=(x, (M, K)),
-            q=(q, (M, K), torch.int8), q_scale=(q_scale, (K // g if g > 0 else 0, M), torch.float32),
-            dx_base=(dx_base, (M, K)), dx=(dx, (M, K)))
+    if dx is None and want_dx:
+        dx = torch.empty((M, K), dtype=dt, device=dy.device)
+    ap, bp = _fit("a", a, (L, R, K), dt, dev), _fit("b", b, (L, N, R), dt, dev)
     da, db = torch.empty_like(a), torch.empty_like(b)
-    ws = _workspace(workspace, adapters_workspace_size(M, N, K, L, R, True), dy.device)
-    with torch.cuda.device(dy.device):
-        _check(lib().qlin_adapters_backward(_ptr(dy), _dt(dy), M, N, _ptr(a), _ptr(b), _ptr(scales), L, R, K,
-                                            _ptr(plan.buffer), plan.buffer.numel(), _ptr(u), _ptr(x), _ptr(q),
-                                            _ptr(q_scale), g, _ptr(dx_base), _ptr(dx), _ptr(da), _ptr(db), _ptr(ws),
-                                            ws.numel(), _stream(dy.device)), "qlin_adapters_backward")
+    ws, wp, wn = _space(workspace, lib().qlin_adapters_workspace_size(M, N, K, L, R, 1), dev, dy)
+    _run("qlin_adapters_backward", dev, _fit("dy", dy, (M, N), dt, dev), _dt(dy), M, N, ap, bp,
+         _fit("scales", scales, (L,), f32, dev), L, R, K, plan.buffer.data_ptr(), plan.buffer.numel(),
+         _fit("u", u, (M, R), f32, dev), _fit("x", x, (M, K), dt, dev), _fit("q", q, (M, K), torch.int8, dev),
+         _fit("q_scale", q_scale, (K // g if g > 0 else 0, M), f32, dev), g, _fit("dx_base", dx_base, (M, K), dt, dev),
+         _fit("dx", dx, (M, K), dt, dev), da.data_ptr(), db.data_ptr(), wp, wn)
     return dx, da, db
 
 
@@ -431,13 +443,12 @@ def dequantize_int8_groups(q, scale, group_size: int, out_dtype=torch.bfloat16, 
     if q.dim() != 2:
         raise ValueError("q must be a matrix")
     N, K = q.shape
+    dev = q.get_device()
     if out is None:
         out = torch.empty((N, K), dtype=out_dtype, device=q.device)
-    _expect(q.device, out_dtype, q=(q, (N, K), torch.int8), out=(out, (N, K)),
-            scale=(scale, (K // group_size if group_size > 0 else 0, N), torch.float32))
-    with torch.cuda.device(q.device):
-        _check(lib().qlin_dequantize_int8_groups(_ptr(q), _ptr(scale), N, K, group_size, _ptr(out), _dt(out),
-                                                 _stream(q.device)), "qlin_dequantize_int8_groups")
+    _run("qlin_dequantize_int8_groups", dev, _fit("q", q, (N, K), torch.int8, dev),
+         _fit("scale", scale, (K // group_size if group_size > 0 else 0, N), torch.float32, dev), N, K, group_size,
+         _fit("out", out, (N, K), out_dtype, dev), _dt(out))
     return out
 
 
@@ -446,13 +457,11 @@ def pergroup_wgrad(dy, q, scale, group_size: int, bias: bool = True, dw=None):
     if dy.dim() != 2 or q.dim() != 2:
         raise ValueError("dy and q must be matrices")
     M, N = dy.shape
-    K = q.shape[1]
+    K, dt, dev = q.shape[1], dy.dtype, dy.get_device()
     if dw is None:
-        dw = torch.empty((N, K), dtype=dy.dtype, device=dy.device)
-    _expect(dy.device, dy.dtype, dy=(dy, (M, N)), q=(q, (M, K), torch.int8), dw=(dw, (N, K)),
-            scale=(scale, (K // group_size if group_size > 0 else 0, M), torch.float32))
-    db = torch.empty((N,), dtype=dy.dtype, device=dy.device) if bias else None
-    with torch.cuda.device(dy.device):
-        _check(lib().pergroup_wgrad(_ptr(dy), _dt(dy), M, N, _ptr(q), _ptr(scale), K, group_size, _ptr(dw), _ptr(db),
-                                    _stream(dy.device)), "pergroup_wgrad")
+        dw = torch.empty((N, K), dtype=dt, device=dy.device)
+    db = torch.empty((N,), dtype=dt, device=dy.device) if bias else None
+    _run("pergroup_wgrad", dev, _fit("dy", dy, (M, N), dt, dev), _dt(dy), M, N, _fit("q", q, (M, K), torch.int8, dev),
+         _fit("scale", scale, (K // group_size if group_size > 0 else 0, M), torch.float32, dev), K, group_size,
+         _fit("dw", dw, (N, K), dt, dev), None if db is None else db.data_ptr())
     return dw, db
