@@ -1,23 +1,27 @@
 // k_adapters_tc.cu -- low-rank adapters on the tensor cores, bf16 and fp16 (sm_100a).
 //
-//   narrow   h[m] = A_i x[m]  (forward)  or  v[m] = s_i B_i^T dy[m]  (backward)      tcgen05
-//   wide     out[m] = base[m] + s_i B_i h[m]   or   dx[m] = dx_base[m] + A_i^T v[m]  mma.sync
-//   grams    dB_i = s_i sum_m dy[m] u[m]^T,  dA_i^T = sum_m x[m] v[m]^T              tcgen05
+//   narrow   h[m] = A_i x[m]  (forward)  or  v[m] = s_i B_i^T dy[m]  (backward)
+//   wide     out[m] = base[m] + s_i B_i h[m]   or   dx[m] = dx_base[m] + A_i^T v[m]
+//   grams    dB_i = s_i sum_m dy[m] u[m]^T,  dA_i^T = sum_m x[m] v[m]^T
+//   decode   both products of the forward pass for few tokens, in one launch
 //
-// All three move one long activation row (or write one) for each token and do 2 R products a
-// value, R <= 128, so memory bounds them: the tensor cores only have to keep up.  Tokens are taken
-// in tiles of 128 of one adapter (the plan's list); a tile's rows lie anywhere in the batch, so
-// they are gathered with 16-byte asynchronous copies (zero-filled past the tile's last token, so
-// nothing of another adapter's rows enters a sum) instead of tensor-map boxes.
+// The first three are tcgen05 kernels.  Each moves one long activation row in (or one in and one
+// out) for every token and does 2 to 4 R products a value, R <= 128, so memory bounds them; the
+// tensor cores and the threads only have to keep up.  Tokens are taken in tiles of 128 of one
+// adapter (the plan's list).  A tile whose tokens are consecutive is read in tensor-map boxes of 64
+// rows, any other by tile::gather4, four rows an instruction: no thread touches the data before
+// the tensor cores (threads with cp.async, 8 copies each a stage, reached 2.2 TB/s; boxes of the
+// same stages are bounded by memory).
 //
-// h and v stay in fp32 between the kernels ([tile][128][Rq], Rq = R rounded up to 16, zero where
-// there is no token or rank) and enter the second product as two 16-bit halves, hi = round(h) and
-// lo = round(h - hi): 2^-16 of the value at most, and two MMAs instead of one.  fp16 halves are
-// scaled by a power of two that puts the largest value of the row (wide) or of the adapter (grams)
-// in [2^14, 2^15), undone on the fp32 sum; bf16 has fp32's range and needs none.
+// h, u and v enter their second product as two 16-bit halves, hi = round(h) and lo = round(h - hi):
+// 2^-16 of the value at most, and two MMAs instead of one.  They are kept in slots, [tile][128][Rq]
+// (Rq = R rounded up to 16), zero where there is no token or rank, hi and lo apart.  fp16 halves
+// are scaled by a power of two that puts the largest value of the row (wide) or of the adapter
+// (grams) in [2^14, 2^15), undone on the fp32 sum; bf16 has fp32's range and needs none.
 //
 // Every mbarrier wait is bounded: on expiry the kernel records the timeout, every role stops, MMAs
 // and copies in flight are waited for and TMEM is freed.
+#include <cstdlib>
 #include <initializer_list>
 
 #include "adapters.cuh"
@@ -29,14 +33,6 @@ constexpr uint32_t kAtom = 64 * 128;  // a 64-row x 128-byte swizzled block
 constexpr int kMaxSplit = 8;          // CTAs of a cluster: the portable size
 
 // ------------------------------------------------------------------------------------ helpers
-
-QLIN_DEV void cp_async16(uint32_t dst, const void* src, bool in)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-}
-QLIN_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-QLIN_DEV void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 QLIN_DEV void cluster_sync()
 {
@@ -63,10 +59,6 @@ QLIN_DEV float ld_peer(uint32_t addr)
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
-}
-QLIN_DEV void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b)
-{
-    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 QLIN_DEV void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
@@ -111,12 +103,59 @@ QLIN_DEV float finite_abs(float v)
 // Sorted-token views that the kernels share.
 struct Common {
     PlanView plan;
-    int64_t M;
+    int64_t M, slots;       // slots: 128 for each tile of the plan's bound
     int L, R, Rq;
-    float* h;         // [tiles of 128][128][Rq]
-    float* tile_max;  // [tiles of 128][kMaxSplit][2]: largest finite |v| and |u| of a CTA's rows (fp16)
+    uint16_t* row_halves;   // [2][slots][Rq]: hi and lo of h (forward) or v, for the wide product
+    uint16_t* v_halves;     // [2][slots][Rq]: of v for the grams (bf16: the same)
+    uint16_t* u_halves;     // [2][slots][Rq]: of u for the grams
+    float* row_back;        // [slots], fp16: what undoes a row's scale
+    float* v;               // [slots][Rq], fp16 backward: v itself
+    float* tile_max;        // [tiles][kMaxSplit][2], fp16 backward: largest finite |v| and |u| of a CTA's rows
     unsigned* status;
 };
+
+// Four rows of a 2-D tensor map (box {64, 1}) into consecutive 128-byte rows.
+QLIN_DEV void tma_gather4(uint32_t dst, const CUtensorMap* tm, int c0, const int4& r, uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// A matrix of token rows: boxes of 64 rows, and single rows for gathers.
+struct RowMaps {
+    CUtensorMap box, row;
+};
+
+// One warp: `64 n64` rows of 64 elements from column c0 (128 bytes of column for bytes), from row
+// `first`, or, where first < 0, rows `r` of each lane (lane l: rows 4 l .. of the block).
+QLIN_DEV void load_rows(uint32_t dst, const RowMaps& m, int c0, int first, const int4& r, int n64, int lane, uint64_t* bar)
+{
+    if (first >= 0) {
+        if (lane == 0)
+            for (int h = 0; h < n64; ++h)
+                asm volatile(
+                    "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+                    "[%1, {%2, %3}], [%4];" ::"r"(dst + h * kAtom),
+                    "l"(reinterpret_cast<uint64_t>(&m.box)), "r"(c0), "r"(first + 64 * h), "r"(smem_u32(bar))
+                    : "memory");
+    } else if (lane < 16 * n64) {
+        tma_gather4(dst + lane * 512, &m.row, c0, r, bar);
+    }
+}
+
+// Tokens of rows 4 lane .. 4 lane + 3 of positions [start, start + count); past the end the first
+// (its row is read and never used, or zeroed).
+QLIN_DEV int4 row_tokens(const PlanView& v, int start, int count, int lane)
+{
+    int t[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        t[e] = v.perm[start + (4 * lane + e < count ? 4 * lane + e : 0)];
+    return make_int4(t[0], t[1], t[2], t[3]);
+}
 
 // ------------------------------------------------------------------------------------ narrow
 
@@ -124,30 +163,31 @@ struct Common {
 // [128][Rq] in tensor memory over its steps of 64; the partial sums meet through distributed shared
 // memory, CTA j adding the parts of rows 128 j / z .. in order, so h is written once and the order
 // of every sum is fixed.
-//   warps 0..3   gather the activation rows (cp.async, 128-byte swizzle), then the epilogue
-//   warp 4       tensor memory, the MMAs (M = 128, N = Rq, K = 16)
-//   warp 5       TMA of the factor: forward A_i [Rq rows][64 k], K-major; backward B_i [64 n][R],
-//                MN-major -- a 3-D map, so that rows and columns past the adapter's own are zeros
-constexpr int kNarrowLag = 3;       // stages whose copies are in flight behind the newest
+//   warp 0       the loads: activation rows, and the factor -- forward A_i [Rq rows][64 k], K-major;
+//                backward B_i [64 n][R], MN-major -- from a 3-D map, so that rows and columns past
+//                the adapter's own are zeros
+//   warp 1       tensor memory, the MMAs (M = 128, N = Rq, K = 16)
+//   warps 2..5   the epilogue
 constexpr int kNarrowThreads = 192;
 constexpr int kNarrowMaxStages = 8;
 
 struct NarrowParams {
+    RowMaps w;            // x [M][K] or dy [M][N]
     CUtensorMap tm_f;
     Common c;
-    const void* w;        // x [M][K] or dy [M][N]
     int64_t K;            // the contraction's length
     int steps;            // 64-wide steps of one CTA
     int stages, f_bytes;  // ring depth, bytes of the factor in a stage
     int tmem_cols;
     const float* scales;  // backward: s
-    const float* u_in;    // backward, fp16: u [M][R], for its maximum
+    const float* u_in;    // backward: u [M][R]
     float* u_out;         // forward: [M][R] or null
 };
 
 template <typename T, bool FWD>
-__global__ void __launch_bounds__(kNarrowThreads) adapters_narrow_tc_kernel(const __grid_constant__ NarrowParams p)
+__global__ void __launch_bounds__(kNarrowThreads) adapters_narrow_kernel(const __grid_constant__ NarrowParams p)
 {
+    constexpr int f16 = Is16<T>::f16;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t full[kNarrowMaxStages], empty[kNarrowMaxStages], acc_full;
@@ -161,7 +201,7 @@ __global__ void __launch_bounds__(kNarrowThreads) adapters_narrow_tc_kernel(cons
 
     if (tid == 0) {
         for (int s = 0; s < p.stages; ++s) {
-            mbar_init(&full[s], 128 + 1);
+            mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
         mbar_init(&acc_full, 1);
@@ -174,14 +214,14 @@ __global__ void __launch_bounds__(kNarrowThreads) adapters_narrow_tc_kernel(cons
         return;  // the whole cluster
     const AdapterTile d = c.plan.tiles_l[t];
     const int rows = 128 / z, row0 = rank * rows;
-    if (d.adapter >= c.L) {  // tokens without an adapter: u is zero, nothing reads their h
+    if (d.adapter >= c.L) {  // tokens without an adapter: u is zero, nothing reads their slots
         if (FWD && p.u_out)
             for (int i = tid; i < rows * c.R; i += kNarrowThreads)
                 if (row0 + i / c.R < d.count)
                     p.u_out[(size_t)c.plan.perm[d.start + row0 + i / c.R] * c.R + i % c.R] = 0.f;
         return;
     }
-    if (warp == 4)
+    if (warp == 1)
         tmem_alloc(&tmem_s, (uint32_t)p.tmem_cols);
     tc_fence_before();
     __syncthreads();
@@ -196,78 +236,34 @@ __global__ void __launch_bounds__(kNarrowThreads) adapters_narrow_tc_kernel(cons
     auto F = [&](int s) { return smem + s * stage_bytes + 2 * kAtom; };
     const int pitch = c.Rq + 4;  // floats: an odd number of 16-byte units, so rows meet all banks
 
-    if (warp < 4) {
-        const T* w = static_cast<const T*>(p.w);
-        const int chunk = tid & 7;
-        int tok[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int row = (tid >> 3) + 16 * j;
-            tok[j] = row < d.count ? c.plan.perm[d.start + row] : -1;
-        }
-        bool ok = true;
-        auto publish = [&](int it) {
-            fence_proxy_async_smem();
-            mbar_arrive(&full[it % p.stages]);
-        };
+    if (warp == 0) {
+        const int4 tok = d.first >= 0 ? make_int4(0, 0, 0, 0) : row_tokens(c.plan, d.start, d.count, lane);
         int it = 0;
         for (; it < n_st; ++it) {
             const int slot = it % p.stages;
-            if (it >= p.stages && !mbar_wait_bounded(&empty[slot], ((it / p.stages) & 1) ^ 1, c.status)) {
-                ok = false;
+            const bool ok = it < p.stages || mbar_wait_bounded(&empty[slot], ((it / p.stages) & 1) ^ 1, c.status);
+            if (__any_sync(0xffffffffu, !ok || aborted(&abort_flag))) {
+                abort_flag = 1;
                 break;
             }
-            const int64_t k = (int64_t)(k_first + it) * 64 + chunk * 8;
-            const uint32_t dst = smem_u32(X(slot));
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const bool in = tok[j] >= 0 && k < p.K;
-                cp_async16(dst + swz128((tid >> 3) + 16 * j, chunk), in ? w + (size_t)tok[j] * p.K + k : w, in);
+            const int k = (k_first + it) * 64;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&full[slot], (unsigned)stage_bytes);
+                if constexpr (FWD) {
+                    tma_load_3d(F(slot), &p.tm_f, k, 0, d.adapter, &full[slot]);
+                } else {
+                    for (int a = 0; a * 64 < c.Rq; ++a)
+                        tma_load_3d(F(slot) + a * kAtom, &p.tm_f, a * 64, k, d.adapter, &full[slot]);
+                }
             }
-            cp_async_commit();
-            if (it >= kNarrowLag) {
-                cp_async_wait<kNarrowLag>();
-                publish(it - kNarrowLag);
-            }
+            __syncwarp();
+            load_rows(smem_u32(X(slot)), p.w, k, d.first, tok, 2, lane, &full[slot]);
         }
-        if (ok) {
-            if (it >= 3) {
-                cp_async_wait<2>();
-                publish(it - 3);
-            }
-            if (it >= 2) {
-                cp_async_wait<1>();
-                publish(it - 2);
-            }
-            if (it >= 1) {
-                cp_async_wait<0>();
-                publish(it - 1);
-            }
-        } else {
-            abort_flag = 1;
-            cp_async_wait<0>();
-        }
-        // this CTA's sums, [128][Rq], into the ring's memory (every copy and MMA is done)
-        const bool sums = n_st > 0 && mbar_wait_bounded(&acc_full, 0, c.status) && !aborted(&abort_flag);
-        tc_fence_after();
-        float* red = reinterpret_cast<float*>(smem) + (size_t)tid * pitch;
-        for (int col = 0; col < c.Rq; col += 16) {
-            uint32_t r[16];
-            if (sums) {
-                tmem_ld16(tmem + (uint32_t)col + ((uint32_t)(32 * warp) << 16), r);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    r[j] = 0u;
-            }
-#pragma unroll
-            for (int j = 0; j < 16; j += 4)
-                *reinterpret_cast<uint4*>(red + col + j) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
-        }
-        tc_fence_before();
-    } else if (warp == 4) {
+        for (int j = it - p.stages < 0 ? 0 : it - p.stages; j < it; ++j)  // no copy may land after the exit
+            mbar_wait_bounded(&full[j % p.stages], (j / p.stages) & 1, c.status);
+    } else if (warp == 1) {
         if (lane == 0) {
-            const uint32_t ty = Is16<T>::f16 ? 0u : (1u << 7) | (1u << 10);
+            const uint32_t ty = f16 ? 0u : (1u << 7) | (1u << 10);
             const uint32_t idesc = (1u << 4) | ty | (FWD ? 0u : 1u << 16) | ((uint32_t)(c.Rq >> 3) << 17) |
                                    ((uint32_t)(128 >> 4) << 24);
             bool ok = true;
@@ -291,96 +287,396 @@ __global__ void __launch_bounds__(kNarrowThreads) adapters_narrow_tc_kernel(cons
             mbar_wait_bounded(&acc_full, 0, c.status);
         }
         __syncwarp();
-    } else if (lane == 0) {
-        int it = 0;
-        for (; it < n_st; ++it) {
-            const int slot = it % p.stages;
-            if ((it >= p.stages && !mbar_wait_bounded(&empty[slot], ((it / p.stages) & 1) ^ 1, c.status)) ||
-                aborted(&abort_flag)) {
-                abort_flag = 1;
-                break;
-            }
-            mbar_arrive_expect_tx(&full[slot], (unsigned)p.f_bytes);
-            const int k = (k_first + it) * 64;
-            if constexpr (FWD) {
-                tma_load_3d(F(slot), &p.tm_f, k, 0, d.adapter, &full[slot]);
+    } else {
+        // this CTA's sums, [128][Rq], into the ring's memory (every MMA, so every copy, is done)
+        const int q = warp & 3;
+        const bool sums = n_st > 0 && mbar_wait_bounded(&acc_full, 0, c.status) && !aborted(&abort_flag);
+        tc_fence_after();
+        float* red = reinterpret_cast<float*>(smem) + (size_t)(32 * q + lane) * pitch;
+        for (int col = 0; col < c.Rq; col += 16) {
+            uint32_t r[16];
+            if (sums) {
+                tmem_ld16(tmem + (uint32_t)col + ((uint32_t)(32 * q) << 16), r);
             } else {
-                for (int a = 0; a * 64 < c.Rq; ++a)
-                    tma_load_3d(F(slot) + a * kAtom, &p.tm_f, a * 64, k, d.adapter, &full[slot]);
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    r[j] = 0u;
             }
+#pragma unroll
+            for (int j = 0; j < 16; j += 4)
+                *reinterpret_cast<uint4*>(red + col + j) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
         }
-        for (int j = it - p.stages < 0 ? 0 : it - p.stages; j < it; ++j)  // no copy may land after the exit
-            mbar_wait_bounded(&full[j % p.stages], (j / p.stages) & 1, c.status);
+        tc_fence_before();
     }
     __syncthreads();
     cluster_sync();
-    if (warp < 4) {
+    if (warp >= 2) {
+        // a warp a row: lane l adds the parts of columns 4 l .. 4 l + 3
         const float sc = FWD ? 1.f : p.scales[d.adapter];
-        const int per = c.Rq / 4;
         const uint32_t mine = smem_u32(smem);
+        const int col = 4 * lane;
+        const size_t lo_at = (size_t)c.slots * c.Rq;
         float vmax = 0.f, umax = 0.f;
-        for (int i = tid; i < rows * per; i += 128) {
-            const int row = row0 + i / per, col = 4 * (i % per);
+        for (int row = row0 + warp - 2; row < row0 + rows; row += 4) {
             const bool in = row < d.count && col < c.R;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int j = 0; j < z; ++j) {
-                const float4 v = ld_peer_v4(peer_smem(mine + (uint32_t)(row * pitch + col) * 4u, (uint32_t)j));
-                s.x += v.x;
-                s.y += v.y;
-                s.z += v.z;
-                s.w += v.w;
+            const size_t at = ((size_t)t * kTileL + row) * c.Rq + col;
+            const size_t tok = in ? (size_t)c.plan.perm[d.start + row] : 0;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f), u = s;
+            if (in && !FWD)
+                u = __ldg(reinterpret_cast<const float4*>(p.u_in + tok * c.R + col));
+            if (in) {
+                for (int j = 0; j < z; ++j) {
+                    const float4 v = ld_peer_v4(peer_smem(mine + (uint32_t)(row * pitch + col) * 4u, (uint32_t)j));
+                    s.x += v.x;
+                    s.y += v.y;
+                    s.z += v.z;
+                    s.w += v.w;
+                }
+                s = make_float4(sc * s.x, sc * s.y, sc * s.z, sc * s.w);
+                if (FWD && p.u_out)
+                    *reinterpret_cast<float4*>(p.u_out + tok * c.R + col) = s;
             }
-            s = in ? make_float4(sc * s.x, sc * s.y, sc * s.z, sc * s.w) : make_float4(0.f, 0.f, 0.f, 0.f);
-            *reinterpret_cast<float4*>(c.h + ((size_t)t * kTileL + row) * c.Rq + col) = s;
-            if (in && FWD && p.u_out)
-                *reinterpret_cast<float4*>(p.u_out + (size_t)c.plan.perm[d.start + row] * c.R + col) = s;
-            if (in && !FWD && Is16<T>::f16) {
-                const float4 u = *reinterpret_cast<const float4*>(p.u_in + (size_t)c.plan.perm[d.start + row] * c.R + col);
-                vmax = fmaxf(fmaxf(vmax, fmaxf(finite_abs(s.x), finite_abs(s.y))), fmaxf(finite_abs(s.z), finite_abs(s.w)));
-                umax = fmaxf(fmaxf(umax, fmaxf(finite_abs(u.x), finite_abs(u.y))), fmaxf(finite_abs(u.z), finite_abs(u.w)));
+            float to = 1.f, back = 1.f;
+            if constexpr (f16) {
+                float top = fmaxf(fmaxf(finite_abs(s.x), finite_abs(s.y)), fmaxf(finite_abs(s.z), finite_abs(s.w)));
+                vmax = fmaxf(vmax, top);
+                umax = fmaxf(umax, fmaxf(fmaxf(finite_abs(u.x), finite_abs(u.y)), fmaxf(finite_abs(u.z), finite_abs(u.w))));
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                half_scale<T>(top, to, back);
+                if (lane == 0)
+                    c.row_back[(size_t)t * kTileL + row] = back;
+            }
+            if (col < c.Rq) {
+                uint2 hi, lo;
+                split2<T>(s.x * to, s.y * to, hi.x, lo.x);
+                split2<T>(s.z * to, s.w * to, hi.y, lo.y);
+                *reinterpret_cast<uint2*>(c.row_halves + at) = hi;
+                *reinterpret_cast<uint2*>(c.row_halves + lo_at + at) = lo;
+                if constexpr (!FWD && f16) {
+                    *reinterpret_cast<float4*>(c.v + at) = s;
+                } else if constexpr (!FWD) {
+                    split2<T>(u.x, u.y, hi.x, lo.x);
+                    split2<T>(u.z, u.w, hi.y, lo.y);
+                    *reinterpret_cast<uint2*>(c.u_halves + at) = hi;
+                    *reinterpret_cast<uint2*>(c.u_halves + lo_at + at) = lo;
+                }
             }
         }
-        if (!FWD && Is16<T>::f16) {
+        if constexpr (!FWD && f16) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
                 vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
                 umax = fmaxf(umax, __shfl_xor_sync(0xffffffffu, umax, o));
             }
             if (lane == 0) {
-                warp_max[0][warp] = vmax;
-                warp_max[1][warp] = umax;
+                warp_max[0][warp - 2] = vmax;
+                warp_max[1][warp - 2] = umax;
             }
             asm volatile("bar.sync 1, 128;" ::: "memory");
-            if (tid < 2)
-                c.tile_max[((size_t)t * kMaxSplit + rank) * 2 + tid] =
-                    fmaxf(fmaxf(warp_max[tid][0], warp_max[tid][1]), fmaxf(warp_max[tid][2], warp_max[tid][3]));
+            if (tid - 64 < 2) {
+                const float* w = warp_max[tid - 64];
+                c.tile_max[((size_t)t * kMaxSplit + rank) * 2 + tid - 64] = fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3]));
+            }
         }
     }
     cluster_sync();  // no CTA's shared memory goes while another reads it
-    if (warp == 4)
+    if (warp == 1)
         tmem_dealloc(tmem, (uint32_t)p.tmem_cols);
+}
+
+// The grams' halves for fp16, scaled by the adapter's power of two: a CTA for each tile.
+struct SplitParams {
+    Common c;
+    const float* u;  // [M][R]
+    int parts;       // CTAs of a tile in the narrow kernel: maxima of a tile
+};
+
+QLIN_DEV float adapter_max(const Common& c, int i, int which, int parts, int lane)
+{
+    float top = 0.f;
+    const int t0 = c.plan.tile_l0[i], n = (c.plan.tile_l0[i + 1] - t0) * parts;
+    for (int e = lane; e < n; e += 32)
+        top = fmaxf(top, c.tile_max[((size_t)(t0 + e / parts) * kMaxSplit + e % parts) * 2 + which]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    return top;
+}
+
+__global__ void __launch_bounds__(256) adapters_split_kernel(const SplitParams p)
+{
+    const Common& c = p.c;
+    pdl_launch_dependents();
+    pdl_wait_prior_grids();
+    const int t = blockIdx.x, lane = threadIdx.x & 31;
+    if (t >= c.plan.head[5])
+        return;
+    const AdapterTile d = c.plan.tiles_l[t];
+    float tov, tou, back;
+    half_scale<__half>(adapter_max(c, d.adapter, 0, p.parts, lane), tov, back);
+    half_scale<__half>(adapter_max(c, d.adapter, 1, p.parts, lane), tou, back);
+    const int per = c.Rq / 4;
+    const size_t lo_at = (size_t)c.slots * c.Rq;
+    for (int i = threadIdx.x; i < kTileL * per; i += 256) {
+        const int row = i / per, col = 4 * (i % per);
+        const size_t at = ((size_t)t * kTileL + row) * c.Rq + col;
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(c.v + at));
+        float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row < d.count && col < c.R)
+            u = __ldg(reinterpret_cast<const float4*>(p.u + (size_t)c.plan.perm[d.start + row] * c.R + col));
+        uint2 hi, lo;
+        split2<__half>(v.x * tov, v.y * tov, hi.x, lo.x);
+        split2<__half>(v.z * tov, v.w * tov, hi.y, lo.y);
+        *reinterpret_cast<uint2*>(c.v_halves + at) = hi;
+        *reinterpret_cast<uint2*>(c.v_halves + lo_at + at) = lo;
+        split2<__half>(u.x * tou, u.y * tou, hi.x, lo.x);
+        split2<__half>(u.z * tou, u.w * tou, hi.y, lo.y);
+        *reinterpret_cast<uint2*>(c.u_halves + at) = hi;
+        *reinterpret_cast<uint2*>(c.u_halves + lo_at + at) = lo;
+    }
 }
 
 // ------------------------------------------------------------------------------------ wide
 
-// out = base + h F on mma.sync m16n8k16: 128 rows of a tile by a strip of columns, each warp 16 MT
-// rows by 64 columns at a time.  The products (2 R 2 for each value, hi and lo) stay below the rate
-// at which memory takes base and out up to R = 64; nothing is staged: the n index of the eight
-// 8-column MMAs is permuted so that a thread ends up with 16 consecutive columns of each row (two
-// 16-byte loads of base, two stores of out; four lanes cover 128 bytes of a row), and the
-// contraction index so that the factor's fragments come straight from memory, 8 bytes of a row of
-// B_i (forward) or 16 of rows of A_i (backward).
-constexpr int kWideWarps = 8;
+// out = base + h F: a CTA for each tile and strip of columns, 128 columns at a time.
+//   warp 0       the loads: once the halves of h; each block's factor -- forward B_i [128 n][R],
+//                K-major; backward A_i [Rq r][128 k], MN-major -- and base [128 rows][128 columns]
+//   warp 1       two accumulators of 128 columns; hi and lo halves on the same factor block
+//   warps 2..9   32 rows by 64 columns each: the sum, scaled, onto base in shared memory, then out in
+//                whole 128-byte pieces of a row (base's own place serves as the staging buffer)
+constexpr int kWideEpi = 8;
+constexpr int kWideThreads = (2 + kWideEpi) * 32;
+constexpr int kWideMaxStages = 4;
+constexpr int kWideCols = 128;
 
 struct WideParams {
+    RowMaps base;
+    CUtensorMap tm_f, tm_h;
     Common c;
-    const void* f;        // b [L][N][R] (forward) or a [L][R][N] (backward)
     const float* scales;  // forward
-    const void* base;
+    const void* base_p;   // null: zeros
     void* out;
     int64_t N;
-    int strip;            // columns of a CTA
+    int strip;            // columns of a CTA, a multiple of 128
+    int stages, f_bytes;
 };
+
+template <typename T, bool FWD>
+__global__ void __launch_bounds__(kWideThreads, 1) adapters_wide_kernel(const __grid_constant__ WideParams p)
+{
+    constexpr int f16 = Is16<T>::f16;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ uint64_t full[kWideMaxStages], empty[kWideMaxStages], acc_full[2], acc_empty[2], h_full;
+    __shared__ uint32_t tmem_s;
+    __shared__ int abort_flag;
+    const Common& c = p.c;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1 + kWideEpi);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], kWideEpi);
+        }
+        mbar_init(&h_full, 1);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    pdl_wait_prior_grids();
+    const int t = blockIdx.y;
+    if (t >= c.plan.head[3])
+        return;
+    const AdapterTile d = c.plan.tiles_l[t];
+    const int64_t n_begin = (int64_t)blockIdx.x * p.strip;
+    const int64_t n_end = n_begin + p.strip < p.N ? n_begin + p.strip : p.N;
+    T* out = static_cast<T*>(p.out);
+    if (d.adapter >= c.L) {
+        if (p.base_p == p.out)
+            return;
+        const T* base = static_cast<const T*>(p.base_p);
+        const int vecs = (int)((n_end - n_begin) / 8);
+        for (int i = tid; i < d.count * vecs; i += kWideThreads) {
+            const size_t at = (size_t)c.plan.perm[d.start + i / vecs] * p.N + n_begin + 8 * (i % vecs);
+            *reinterpret_cast<uint4*>(out + at) =
+                base ? *reinterpret_cast<const uint4*>(base + at) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        return;
+    }
+    if (warp == 1)
+        tmem_alloc(&tmem_s, 2 * kWideCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_launch_dependents();  // after the allocation, as in the narrow kernel
+    const uint32_t tmem = tmem_s;
+    const int blocks = (int)((n_end - n_begin + kWideCols - 1) / kWideCols);
+    const int atoms = (c.Rq + 63) / 64, h_half = atoms * 2 * (int)kAtom;
+    constexpr int base_bytes = 4 * (int)kAtom;
+    const int stage_bytes = base_bytes + p.f_bytes;
+    uint8_t* Hs = smem;  // hi, then lo: [atoms][128 rows][128 bytes]
+    auto B = [&](int s) { return smem + 2 * h_half + s * stage_bytes; };
+    auto F = [&](int s) { return smem + 2 * h_half + s * stage_bytes + base_bytes; };
+
+    if (warp == 0) {
+        const int4 tok = d.first >= 0 ? make_int4(0, 0, 0, 0) : row_tokens(c.plan, d.start, d.count, lane);
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&h_full, 2u * (unsigned)h_half);
+            for (int half = 0; half < 2; ++half)
+                for (int a = 0; a < atoms; ++a)
+                    tma_load_2d(Hs + half * h_half + a * 2 * kAtom, &p.tm_h, a * 64, (int)(half * c.slots) + t * kTileL, &h_full);
+        }
+        int it = 0;
+        for (; it < blocks; ++it) {
+            const int slot = it % p.stages;
+            const bool ok = it < p.stages || mbar_wait_bounded(&empty[slot], ((it / p.stages) & 1) ^ 1, c.status);
+            if (__any_sync(0xffffffffu, !ok || aborted(&abort_flag))) {
+                abort_flag = 1;
+                break;
+            }
+            const int n = (int)n_begin + it * kWideCols;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&full[slot], (unsigned)(p.f_bytes + (p.base_p ? base_bytes : 0)));
+                if constexpr (FWD) {
+                    for (int a = 0; a < atoms; ++a)
+                        tma_load_3d(F(slot) + a * 2 * kAtom, &p.tm_f, a * 64, n, d.adapter, &full[slot]);
+                } else {
+                    for (int a = 0; a < 2; ++a)
+                        tma_load_3d(F(slot) + a * c.Rq * 128, &p.tm_f, n + a * 64, 0, d.adapter, &full[slot]);
+                }
+            }
+            __syncwarp();
+            if (p.base_p)
+                for (int a = 0; a < 2; ++a)
+                    load_rows(smem_u32(B(slot)) + a * 2 * kAtom, p.base, n + a * 64, d.first, tok, 2, lane, &full[slot]);
+        }
+        mbar_wait_bounded(&h_full, 0, c.status);
+        for (int j = it - p.stages < 0 ? 0 : it - p.stages; j < it; ++j)
+            mbar_wait_bounded(&full[j % p.stages], (j / p.stages) & 1, c.status);
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t ty = f16 ? 0u : (1u << 7) | (1u << 10);
+            const uint32_t idesc = (1u << 4) | ty | (FWD ? 0u : 1u << 16) | ((uint32_t)(kWideCols >> 3) << 17) |
+                                   ((uint32_t)(128 >> 4) << 24);
+            bool ok = mbar_wait_bounded(&h_full, 0, c.status);
+            int last = -1;
+            for (int it = 0; it < blocks && ok; ++it) {
+                const int slot = it % p.stages, buf = it & 1;
+                ok = mbar_wait_bounded(&acc_empty[buf], ((it >> 1) & 1) ^ 1, c.status) &&
+                     mbar_wait_bounded(&full[slot], (it / p.stages) & 1, c.status);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                const uint32_t h = smem_u32(Hs), f = smem_u32(F(slot));
+                for (int kk = 0; kk < c.Rq / 16; ++kk) {
+                    const uint64_t fd = FWD ? umma_desc_sw128(f + (kk >> 2) * 2 * kAtom + (kk & 3) * 32)
+                                            : umma_desc_sw128_mn(f + kk * 2048, (uint32_t)(c.Rq * 128));
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+                        tc_mma<false>(tmem + (uint32_t)(buf * kWideCols),
+                                      umma_desc_sw128(h + half * h_half + (kk >> 2) * 2 * kAtom + (kk & 3) * 32), fd,
+                                      idesc, (kk | half) != 0 ? 1u : 0u);
+                }
+                tc_commit(&empty[slot]);
+                tc_commit(&acc_full[buf]);
+                last = it;
+            }
+            if (!ok)
+                abort_flag = 1;
+            if (last >= 0)  // every MMA issued has completed before TMEM is released
+                mbar_wait_bounded(&acc_full[last & 1], (last >> 1) & 1, c.status);
+        }
+        __syncwarp();
+    } else {
+        const int q = warp & 3, half = (warp - 2) >> 2, row = 32 * q + lane;
+        const int my_tok = row < d.count ? c.plan.perm[d.start + row] : -1;
+        float rs = FWD ? p.scales[d.adapter] : 1.f;
+        if constexpr (f16)
+            rs *= __ldcg(c.row_back + (size_t)t * kTileL + row);
+        for (int it = 0; it < blocks; ++it) {
+            const int slot = it % p.stages, buf = it & 1;
+            if (!mbar_wait_bounded(&full[slot], (it / p.stages) & 1, c.status) ||
+                !mbar_wait_bounded(&acc_full[buf], (it >> 1) & 1, c.status) || aborted(&abort_flag)) {
+                abort_flag = 1;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t acc = tmem + (uint32_t)(buf * kWideCols + half * 64) + ((uint32_t)(32 * q) << 16);
+            uint8_t* at = B(slot) + half * 2 * kAtom;
+            uint32_t r[4][16];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                tmem_ld16_nowait(acc + 16u * e, r[e]);
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&acc_empty[buf]);
+#pragma unroll
+            for (int un = 0; un < 8; ++un) {
+                uint4* b = reinterpret_cast<uint4*>(at + swz128(row, un));
+                const uint4 bv = p.base_p ? *b : make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t bw[4] = {bv.x, bv.y, bv.z, bv.w};
+                uint32_t o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[e] = pack_h16x2(
+                        fmaf(__uint_as_float(r[un >> 1][(un & 1) * 8 + 2 * e]), rs, h16_to_float(bw[e], f16)),
+                        fmaf(__uint_as_float(r[un >> 1][(un & 1) * 8 + 2 * e + 1]), rs, h16_to_float(bw[e] >> 16, f16)), f16);
+                *b = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            __syncwarp();
+            const int64_t n = n_begin + it * kWideCols + half * 64 + 8 * (lane & 7);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int rr = 4 * e + (lane >> 3);
+                const int tok = __shfl_sync(0xffffffffu, my_tok, rr);
+                const uint4 v = *reinterpret_cast<const uint4*>(at + swz128(32 * q + rr, lane & 7));
+                if (tok >= 0 && n < p.N)
+                    *reinterpret_cast<uint4*>(out + (size_t)tok * p.N + n) = v;
+            }
+            fence_proxy_async_smem();  // the next copy into this place comes after these accesses
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&empty[slot]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1)
+        tmem_dealloc(tmem, 2 * kWideCols);
+}
+
+// ------------------------------------------------------------------------------------ decode
+
+// Both products in one launch, for few tokens: a cluster for each tile of 8 tokens of one adapter.
+// Latency bounds it (one token of a 4096 x 4096 layer at rank 16 reads 0.26 MB), so everything a
+// warp needs is requested at once, straight into MMA fragments: ranks are the MMA's 16 rows, tokens
+// its 8 columns, and the contraction index is permuted so that a fragment is 16 contiguous bytes of
+// a row of A_i or x.  The CTAs split the contraction; each sends its sums [Rq][8] to every CTA of
+// the cluster (one barrier), and takes its share of the 128-column blocks of the second product,
+// whose factor it has prefetched into L2 meanwhile.
+constexpr int kDecodeWarps = 8;
+
+struct DecodeParams {
+    Common c;
+    const void* x;
+    const void* a;
+    const void* b;
+    const float* scales;
+    const void* base;
+    void* out;
+    float* u;
+    int64_t K, N;
+};
+
+QLIN_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+QLIN_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+QLIN_DEV void st_peer(uint32_t addr, float v) { asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory"); }
 
 template <typename T>
 QLIN_DEV void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -393,145 +689,192 @@ QLIN_DEV void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint
         mma_bf16_16816(d, a, b0, b1);
 }
 
-template <typename T, bool FWD, int KT, int MT>
-__global__ void __launch_bounds__(kWideWarps * 32) adapters_wide_tc_kernel(const WideParams p)
+template <typename T, int KT>
+__global__ void __launch_bounds__(kDecodeWarps * 32) adapters_decode_kernel(const DecodeParams p)
 {
-    constexpr int f16 = Is16<T>::f16, kRows = 16 * MT;
+    constexpr int f16 = Is16<T>::f16, RQ = 16 * KT, kUnroll = KT <= 2 ? 4 : KT == 4 ? 2 : 1;
+    extern __shared__ __align__(16) float sm[];
     const Common& c = p.c;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane >> 2, q4 = lane & 3;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, j = lane >> 2, q4 = lane & 3;
+    const int z = gridDim.x, rank = blockIdx.x;
+    float* red = sm;                            // [warps][RQ][8]
+    float* recv = red + kDecodeWarps * RQ * 8;  // [z][RQ][8]
+    float* us = recv + z * RQ * 8;              // [8][RQ + 4]
     pdl_launch_dependents();
     pdl_wait_prior_grids();
     const int t = blockIdx.y;
-    if (t >= c.plan.head[3])
-        return;
-    const AdapterTile d = c.plan.tiles_l[t];
-    const int64_t n_begin = (int64_t)blockIdx.x * p.strip;
-    const int64_t n_end = n_begin + p.strip < p.N ? n_begin + p.strip : p.N;
+    if (t >= c.plan.head[2])
+        return;  // the whole cluster
+    const AdapterTile d = c.plan.tiles_s[t];
     const T* base = static_cast<const T*>(p.base);
     T* out = static_cast<T*>(p.out);
+    const int blocks_n = (int)((p.N + 127) / 128);
     if (d.adapter >= c.L) {
-        if (base == out)
-            return;
-        const int vecs = (int)((n_end - n_begin) / 8);
-        for (int i = threadIdx.x; i < d.count * vecs; i += kWideWarps * 32) {
-            const size_t at = (size_t)c.plan.perm[d.start + i / vecs] * p.N + n_begin + 8 * (i % vecs);
-            *reinterpret_cast<uint4*>(out + at) =
-                base ? *reinterpret_cast<const uint4*>(base + at) : make_uint4(0u, 0u, 0u, 0u);
-        }
+        const int vecs = (int)(p.N / 8);
+        if (base != out)
+            for (int i = rank * 256 + tid; i < d.count * vecs; i += z * 256) {
+                const size_t at = (size_t)c.plan.perm[d.start + i / vecs] * p.N + 8 * (i % vecs);
+                *reinterpret_cast<uint4*>(out + at) =
+                    base ? *reinterpret_cast<const uint4*>(base + at) : make_uint4(0u, 0u, 0u, 0u);
+            }
+        if (p.u && rank == 0)
+            for (int i = tid; i < d.count * c.R; i += 256)
+                p.u[(size_t)c.plan.perm[d.start + i / c.R] * c.R + i % c.R] = 0.f;
         return;
     }
-    // the tile's row groups over the warps, the rest of the warps over the columns
-    const int groups = (d.count + kRows - 1) / kRows, subs = kWideWarps / groups;
-    const int g = warp % groups, sub = warp / groups;
-    if (sub >= subs)
-        return;
-    int tok[MT][2];
-    uint32_t hi[MT][KT][4], lo[MT][KT][4];
-    float rs[MT][2];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int row = g * kRows + m * 16 + j + 8 * e;
-            tok[m][e] = row < d.count ? c.plan.perm[d.start + row] : -1;
-            const float* h = c.h + ((size_t)t * kTileL + row) * c.Rq;
-            float4 v[KT];
-            float top = 0.f;
-#pragma unroll
-            for (int k = 0; k < KT; ++k) {
-                v[k] = 16 * k < c.Rq ? __ldcg(reinterpret_cast<const float4*>(h + 16 * k + 4 * q4))
-                                     : make_float4(0.f, 0.f, 0.f, 0.f);
-                top = fmaxf(fmaxf(top, fmaxf(finite_abs(v[k].x), finite_abs(v[k].y))),
-                            fmaxf(finite_abs(v[k].z), finite_abs(v[k].w)));
-            }
-            float to = 1.f, back = 1.f;
-            if constexpr (f16) {
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                half_scale<T>(top, to, back);
-            }
-            rs[m][e] = FWD ? back * p.scales[d.adapter] : back;
-#pragma unroll
-            for (int k = 0; k < KT; ++k) {
-                split2<T>(v[k].x * to, v[k].y * to, hi[m][k][e], lo[m][k][e]);
-                split2<T>(v[k].z * to, v[k].w * to, hi[m][k][2 + e], lo[m][k][2 + e]);
-            }
+    cluster_arrive();  // every CTA of the cluster has started before one writes to another
+    const T* fb = static_cast<const T*>(p.b) + (size_t)d.adapter * p.N * c.R;
+    {
+        // this CTA's blocks of the second factor: 128 R elements each, every z-th block
+        const int lines = 128 * c.R * (int)sizeof(T) / 128;
+        const char* end = reinterpret_cast<const char*>(fb + (size_t)p.N * c.R);
+        const int mine = blocks_n > rank ? (blocks_n - 1 - rank) / z + 1 : 0;
+        for (int i = tid; i < mine * lines && i < 4 * 256; i += 256) {
+            const char* at = reinterpret_cast<const char*>(fb) +
+                             ((size_t)(rank + (i / lines) * z) * lines + i % lines) * 128;
+            if (at < end)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
         }
-    const T* f = static_cast<const T*>(p.f) + (size_t)d.adapter * p.N * c.R;
-    for (int64_t nb = n_begin + 64 * sub; nb < n_end; nb += 64 * subs) {
-        const int64_t n = nb + 16 * q4;  // this thread's 16 columns
-        uint4 bv[MT][2][2];
+    }
+    // ---- A_i x: ranks are MMA rows, tokens columns
+    const int steps = (int)((p.K + 31) / 32), per = (steps + z - 1) / z;
+    const int s1 = min(steps, (rank + 1) * per);
+    const T* xr = static_cast<const T*>(p.x);
+    const int my_tok = j < d.count ? c.plan.perm[d.start + j] : -1;
+    if (my_tok >= 0)
+        xr += (size_t)my_tok * p.K;
+    const T* fa = static_cast<const T*>(p.a) + (size_t)d.adapter * c.R * p.K;
+    float acc[KT][4] = {};
+    for (int s = rank * per + warp; s < s1; s += kDecodeWarps * kUnroll) {
+        uint4 xv[kUnroll], av[kUnroll][KT][2];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int e = 0; e < kUnroll; ++e) {
+            const int64_t k = (int64_t)(s + e * kDecodeWarps) * 32 + 8 * q4;
+            const bool in = s + e * kDecodeWarps < s1 && k < p.K;
+            xv[e] = in && my_tok >= 0 ? ldg_cg_v4(xr + k) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+            for (int m = 0; m < KT; ++m)
 #pragma unroll
-                for (int v = 0; v < 2; ++v)
-                    bv[m][e][v] = base && tok[m][e] >= 0 && n + 8 * v < p.N
-                                      ? *reinterpret_cast<const uint4*>(base + (size_t)tok[m][e] * p.N + n + 8 * v)
-                                      : make_uint4(0u, 0u, 0u, 0u);
-        float acc[MT][8][4] = {};
-        // fragment column j of MMA q is column nb + 8 j + q
-        if constexpr (FWD) {
+                for (int h = 0; h < 2; ++h) {
+                    const int r = 16 * m + j + 8 * h;
+                    av[e][m][h] = in && r < c.R ? ldg_stream_v4(fa + (size_t)r * p.K + k) : make_uint4(0u, 0u, 0u, 0u);
+                }
+        }
+#pragma unroll
+        for (int e = 0; e < kUnroll; ++e)
+#pragma unroll
+            for (int m = 0; m < KT; ++m) {
+                const uint32_t a0[4] = {av[e][m][0].x, av[e][m][1].x, av[e][m][0].y, av[e][m][1].y};
+                const uint32_t a1[4] = {av[e][m][0].z, av[e][m][1].z, av[e][m][0].w, av[e][m][1].w};
+                mma_16816<T>(acc[m], a0, xv[e].x, xv[e].y);
+                mma_16816<T>(acc[m], a1, xv[e].z, xv[e].w);
+            }
+    }
+#pragma unroll
+    for (int m = 0; m < KT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<float2*>(red + (warp * RQ + 16 * m + j + 8 * h) * 8 + 2 * q4) =
+                make_float2(acc[m][2 * h], acc[m][2 * h + 1]);
+    __syncthreads();
+    cluster_wait();
+    for (int i = tid; i < RQ * 8; i += 256) {
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kDecodeWarps; ++w)
+            sum += red[w * RQ * 8 + i];
+        const uint32_t at = smem_u32(recv + rank * RQ * 8 + i);
+        for (int k = 0; k < z; ++k)
+            st_peer(peer_smem(at, (uint32_t)k), sum);
+    }
+    cluster_sync();
+    for (int i = tid; i < RQ * 8; i += 256) {
+        float sum = 0.f;
+        for (int k = 0; k < z; ++k)
+            sum += recv[k * RQ * 8 + i];
+        const int r = i >> 3, tok = i & 7;
+        const bool in = tok < d.count && r < c.R;
+        us[tok * (RQ + 4) + r] = in ? sum : 0.f;
+        if (p.u && rank == 0 && in)
+            p.u[(size_t)c.plan.perm[d.start + tok] * c.R + r] = sum;
+    }
+    __syncthreads();
+    // ---- B_i u: columns n are MMA rows (row j of MMA q is column 8 j + q of the block, row j + 8
+    // is 64 columns on), tokens columns
+    uint32_t hi[KT][2], lo[KT][2];
+    float4 v[KT];
+    float top = 0.f, to = 1.f, back = 1.f;
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+        v[k] = *reinterpret_cast<const float4*>(us + j * (RQ + 4) + 16 * k + 4 * q4);
+        top = fmaxf(fmaxf(top, fmaxf(finite_abs(v[k].x), finite_abs(v[k].y))),
+                    fmaxf(finite_abs(v[k].z), finite_abs(v[k].w)));
+    }
+    if constexpr (f16) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        half_scale<T>(top, to, back);
+    }
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+        split2<T>(v[k].x * to, v[k].y * to, hi[k][0], lo[k][0]);
+        split2<T>(v[k].z * to, v[k].w * to, hi[k][1], lo[k][1]);
+    }
+    const float sc = p.scales[d.adapter];
+    float rs[2];
+    int tok[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {  // this thread's two tokens of the sums
+        rs[e] = sc * __shfl_sync(0xffffffffu, back, 4 * (2 * q4 + e));
+        tok[e] = __shfl_sync(0xffffffffu, my_tok, 4 * (2 * q4 + e));
+    }
+    for (int blk = rank + z * warp; blk < blocks_n; blk += z * kDecodeWarps) {
+        const int64_t nb = (int64_t)blk * 128;
+        uint4 bv[2][2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t n = nb + 64 * h + 8 * j;
+                bv[e][h] = base && tok[e] >= 0 && n < p.N
+                               ? *reinterpret_cast<const uint4*>(base + (size_t)tok[e] * p.N + n)
+                               : make_uint4(0u, 0u, 0u, 0u);
+            }
+        float o[8][4] = {};
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+            const bool rin = 16 * k + 4 * q4 < c.R;
+            uint2 f[8][2];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t n = nb + 64 * h + 8 * j + q;
+                    f[q][h] = rin && n < p.N ? __ldg(reinterpret_cast<const uint2*>(fb + (size_t)n * c.R + 16 * k + 4 * q4))
+                                             : make_uint2(0u, 0u);
+                }
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                const int64_t col = nb + 8 * j + q;
-                const T* fr = f + (size_t)col * c.R + 4 * q4;
-#pragma unroll
-                for (int k = 0; k < KT; ++k) {
-                    uint2 b = make_uint2(0u, 0u);
-                    if (col < p.N && 16 * k + 4 * q4 < c.R)
-                        b = __ldg(reinterpret_cast<const uint2*>(fr + 16 * k));
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        mma_16816<T>(acc[m][q], hi[m][k], b.x, b.y);
-                        mma_16816<T>(acc[m][q], lo[m][k], b.x, b.y);
-                    }
-                }
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < KT; ++k) {
-                uint32_t w[4][4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 16 * k + 4 * q4 + i;
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < c.R && nb + 8 * j < p.N)
-                        v = __ldg(reinterpret_cast<const uint4*>(f + (size_t)r * p.N + nb + 8 * j));
-                    w[i][0] = v.x;
-                    w[i][1] = v.y;
-                    w[i][2] = v.z;
-                    w[i][3] = v.w;
-                }
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const uint32_t sel = q & 1 ? 0x7632u : 0x5410u;
-                    const uint32_t b0 = prmt(w[0][q >> 1], w[1][q >> 1], sel), b1 = prmt(w[2][q >> 1], w[3][q >> 1], sel);
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        mma_16816<T>(acc[m][q], hi[m][k], b0, b1);
-                        mma_16816<T>(acc[m][q], lo[m][k], b0, b1);
-                    }
-                }
+                const uint32_t a[4] = {f[q][0].x, f[q][1].x, f[q][0].y, f[q][1].y};
+                mma_16816<T>(o[q], a, hi[k][0], hi[k][1]);
+                mma_16816<T>(o[q], a, lo[k][0], lo[k][1]);
             }
         }
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+            for (int h = 0; h < 2; ++h) {
+                const int64_t n = nb + 64 * h + 8 * j;
+                if (tok[e] < 0 || n >= p.N)
+                    continue;
+                const uint32_t bw[4] = {bv[e][h].x, bv[e][h].y, bv[e][h].z, bv[e][h].w};
+                uint32_t w[4];
 #pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    if (tok[m][e] < 0 || n + 8 * v >= p.N)
-                        continue;
-                    const uint32_t bw[4] = {bv[m][e][v].x, bv[m][e][v].y, bv[m][e][v].z, bv[m][e][v].w};
-                    uint32_t o[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        o[q] = pack_h16x2(fmaf(acc[m][2 * q][2 * e + v], rs[m][e], h16_to_float(bw[q], f16)),
-                                          fmaf(acc[m][2 * q + 1][2 * e + v], rs[m][e], h16_to_float(bw[q] >> 16, f16)), f16);
-                    *reinterpret_cast<uint4*>(out + (size_t)tok[m][e] * p.N + n + 8 * v) = make_uint4(o[0], o[1], o[2], o[3]);
-                }
+                for (int q = 0; q < 4; ++q)
+                    w[q] = pack_h16x2(fmaf(o[2 * q][2 * h + e], rs[e], h16_to_float(bw[q], f16)),
+                                      fmaf(o[2 * q + 1][2 * h + e], rs[e], h16_to_float(bw[q] >> 16, f16)), f16);
+                *reinterpret_cast<uint4*>(out + (size_t)tok[e] * p.N + n) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
     }
 }
 
@@ -539,57 +882,58 @@ __global__ void __launch_bounds__(kWideWarps * 32) adapters_wide_tc_kernel(const
 
 // One cluster for each adapter and strip of 256 columns of dy or x: D[256][Rq] = S^T H over the
 // adapter's tokens, 64 at a time, the steps dealt round the cluster's CTAs.  S (dy, x or the
-// restored x) and H (u or v, hi and lo) lie token by token in shared memory, which is MN-major for
-// both operands; nothing is transposed.
-//   warps 0..7   gather S (cp.async; codes: 16-byte loads, s q rounded once to the operand type)
-//                and H (fp32, split), then the epilogue
-//   warp 8       tensor memory, the MMAs (two of M = 128 for hi and for lo, N = Rq, K = 16)
-constexpr int kGramProducers = 256;
-constexpr int kGramThreads = kGramProducers + 32;
-constexpr int kGramStages = 3;
+// restored x) and H (the halves of u or v) lie token by token in shared memory, which is MN-major
+// for both operands; nothing is transposed.
+//   warp 0       the loads: S in 64-column boxes or gathers (codes: 128-byte ones), H in 64-rank boxes
+//   warp 1       tensor memory, the MMAs (two of M = 128 for hi and for lo, N = Rq, K = 16)
+//   warps 2..9   codes: s q in fp32, rounded once to the operand type, into a ring of two buffers;
+//                rows past the adapter's last token: zeros (only there, so what another adapter's
+//                row holds enters no sum); then the epilogue
+constexpr int kGramWork = 8;
+constexpr int kGramThreads = (2 + kGramWork) * 32;
+constexpr int kGramMaxStages = 6;
 
 struct GramParams {
+    RowMaps dy, x;         // x: 16-bit, or the codes
+    CUtensorMap tm_u, tm_v;
     Common c;
-    const void* dy;        // [M][N]
-    const float* u;        // [M][R]
     const float* scales;
-    const void* x;         // [M][K], or
-    const int8_t* q;       // [M][K] with
-    const float* q_scale;  // [K/g][M]
+    const float* q_scale;  // [K/g][M]; null: x is not codes
     int g_shift;
     int64_t N, K;
     int strips_y, strips_x;
     void* da;  // [L][R][K]
     void* db;  // [L][N][R]
     int parts;  // CTAs of a tile in the narrow kernel: maxima of a tile
-    int tmem_cols;
+    int tmem_cols, room;  // room: bytes of shared memory for the rings
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kGramThreads) adapters_gram_kernel(const GramParams p)
+__global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __grid_constant__ GramParams p)
 {
     constexpr int f16 = Is16<T>::f16;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t full[kGramStages], empty[kGramStages], acc_full;
+    __shared__ uint64_t full[kGramMaxStages], empty[kGramMaxStages], ready[2], taken[2], acc_full;
     __shared__ uint32_t tmem_s;
     __shared__ int abort_flag;
-    __shared__ int toks[3][64];
     const Common& c = p.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int z = gridDim.x, rank = blockIdx.x;
-    const int atoms_h = (c.Rq + 63) / 64;
-    const int h_bytes = atoms_h * (int)kAtom, stage_bytes = 4 * (int)kAtom + 2 * h_bytes;
     if (tid == 0) {
-        for (int s = 0; s < kGramStages; ++s) {
-            mbar_init(&full[s], kGramProducers);
+        for (int s = 0; s < kGramMaxStages; ++s) {
+            mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&ready[b], kGramWork);
+            mbar_init(&taken[b], 1);
         }
         mbar_init(&acc_full, 1);
         abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 8)
+    if (warp == 1)
         tmem_alloc(&tmem_s, (uint32_t)p.tmem_cols);
     tc_fence_before();
     __syncthreads();
@@ -600,168 +944,184 @@ __global__ void __launch_bounds__(kGramThreads) adapters_gram_kernel(const GramP
 
     const int strips = p.strips_y + p.strips_x;
     const int i = blockIdx.y / strips, strip = blockIdx.y % strips;
-    const bool of_dy = strip < p.strips_y, of_q = !of_dy && p.q;
+    const bool of_dy = strip < p.strips_y, of_q = !of_dy && p.q_scale;
     const int64_t n0 = (int64_t)(of_dy ? strip : strip - p.strips_y) * 256, ncols = of_dy ? p.N : p.K;
-    const int seg0 = c.plan.seg[i], tokens = c.plan.seg[i + 1] - seg0;
-    const size_t slot0 = (size_t)c.plan.tile_l0[i] * kTileL;
+    const int seg0 = c.plan.seg[i], tokens = c.plan.seg[i + 1] - seg0, tile0 = c.plan.tile_l0[i];
     const int steps = (tokens + 63) / 64;
     const int n_st = steps > rank ? (steps - 1 - rank) / z + 1 : 0;  // steps rank, rank + z, ...
-    auto S = [&](int s) { return smem + s * stage_bytes; };
-    auto H = [&](int s) { return smem + s * stage_bytes + 4 * kAtom; };
-    float to = 1.f, back = 1.f;
-    if constexpr (f16) {
-        float top = 0.f;
-        const int tiles = c.plan.tile_l0[i + 1] - c.plan.tile_l0[i];
-        for (int e = lane; e < tiles * p.parts; e += 32)
-            top = fmaxf(top, c.tile_max[((size_t)(c.plan.tile_l0[i] + e / p.parts) * kMaxSplit + e % p.parts) * 2 +
-                                        (of_dy ? 1 : 0)]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        half_scale<T>(top, to, back);
-    }
+    const int h_half = (c.Rq + 63) / 64 * (int)kAtom;
+    const int src_bytes = of_q ? 2 * (int)kAtom : 4 * (int)kAtom, stage_bytes = src_bytes + 2 * h_half;
+    const int ring = of_q ? 2 * 4 * (int)kAtom : 0;  // decoded buffers, first in shared memory
+    const int stages = min(kGramMaxStages, (p.room - ring) / stage_bytes);
+    auto S = [&](int s) { return smem + ring + s * stage_bytes; };
+    auto H = [&](int s) { return smem + ring + s * stage_bytes + src_bytes; };
+    auto D = [&](int b) { return smem + b * 4 * kAtom; };
+    auto rows_of = [&](int it) { return min(64, tokens - (rank + it * z) * 64); };
+    // a step waits for the worker warps where there is something to decode or to clear
+    auto worked = [&](int it) { return of_q || rows_of(it) < 64; };
 
-    if (warp < 8) {
-        const T* src = static_cast<const T*>(of_dy ? p.dy : p.x);
-        const int per = c.Rq / 4;                        // 16-byte pieces of a row of H
-        const int pieces = 64 * per;                     // <= 8 a thread
-        auto first_of = [&](int it) { return (rank + it * z) * 64; };
-        auto token_at = [&](int it, int row) {
-            const int pos = first_of(it) + row;
-            return it < n_st && pos < tokens ? c.plan.perm[seg0 + pos] : -1;
-        };
-        if (tid < 64) {
-            toks[0][tid] = token_at(0, tid);
-            toks[1][tid] = token_at(1, tid);
-        }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        float4 hv[8];
-        uint4 qv[4];
-        float qs[4];
-        auto load_regs = [&](int it) {  // H and the codes of step it
-            const int* tk = toks[it % 3];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int idx = tid + 256 * e;
-                hv[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (idx < pieces) {
-                    const int row = idx / per, col = 4 * (idx % per), m = tk[row];
-                    if (m >= 0 && col < c.R)
-                        hv[e] = of_dy ? __ldg(reinterpret_cast<const float4*>(p.u + (size_t)m * c.R + col))
-                                      : __ldcg(reinterpret_cast<const float4*>(c.h + (slot0 + first_of(it) + row) * c.Rq + col));
-                }
-            }
-            if (of_q) {
-                const int64_t n = n0 + 16 * (tid & 15);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int m = tk[(tid >> 4) + 16 * e];
-                    const bool in = m >= 0 && n < ncols;
-                    qv[e] = in ? ldg_stream_v4(p.q + (size_t)m * p.K + n) : make_uint4(0u, 0u, 0u, 0u);
-                    qs[e] = in ? __ldg(p.q_scale + (n >> p.g_shift) * c.M + m) : 0.f;
-                }
-            }
-        };
-        auto publish = [&](int it) {
-            fence_proxy_async_smem();
-            mbar_arrive(&full[it % kGramStages]);
-        };
-        if (n_st > 0)
-            load_regs(0);
-        bool ok = true;
+    if (warp == 0) {
+        const RowMaps& m = of_dy ? p.dy : p.x;
         int it = 0;
         for (; it < n_st; ++it) {
-            const int slot = it % kGramStages;
-            const int next = tid < 64 ? token_at(it + 2, tid) : 0;
-            if (ok && it >= kGramStages)
-                ok = mbar_wait_bounded(&empty[slot], ((it / kGramStages) & 1) ^ 1, c.status);
+            const int slot = it % stages, step = rank + it * z;
+            const AdapterTile d = c.plan.tiles_l[tile0 + (step >> 1)];
+            const int first = d.first >= 0 ? d.first + (step & 1) * 64 : -1;
+            const int4 tok = row_tokens(c.plan, seg0 + step * 64, rows_of(it), lane & 15);
+            const bool ok = it < stages || mbar_wait_bounded(&empty[slot], ((it / stages) & 1) ^ 1, c.status);
+            if (__any_sync(0xffffffffu, !ok || aborted(&abort_flag))) {
+                abort_flag = 1;
+                break;
+            }
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&full[slot], (unsigned)stage_bytes);
+                const int slot0 = (tile0 + (step >> 1)) * kTileL + (step & 1) * 64;
+                for (int half = 0; half < 2; ++half)
+                    for (int a = 0; a * 64 < c.Rq; ++a)
+                        tma_load_2d(H(slot) + half * h_half + a * kAtom, of_dy ? &p.tm_u : &p.tm_v, a * 64,
+                                    (int)(half * c.slots) + slot0, &full[slot]);
+            }
+            __syncwarp();
+            const uint32_t s0 = smem_u32(S(slot));
+            if (first >= 0) {
+                for (int a = 0; a * (int)kAtom < src_bytes; ++a)
+                    load_rows(s0 + a * kAtom, m, (int)n0 + a * (of_q ? 128 : 64), first, tok, 1, lane, &full[slot]);
+            } else {  // two blocks of 64 rows at a time, a half of the warp each
+                for (int a = lane >> 4; a * (int)kAtom < src_bytes; a += 2)
+                    tma_gather4(s0 + a * kAtom + (lane & 15) * 512, &m.row, (int)n0 + a * (of_q ? 128 : 64), tok, &full[slot]);
+            }
+        }
+        for (int j = it - stages < 0 ? 0 : it - stages; j < it; ++j)
+            mbar_wait_bounded(&full[j % stages], (j / stages) & 1, c.status);
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t ty = f16 ? 0u : (1u << 7) | (1u << 10);
+            const uint32_t idesc = (1u << 4) | ty | (1u << 15) | (1u << 16) | ((uint32_t)(c.Rq >> 3) << 17) |
+                                   ((uint32_t)(128 >> 4) << 24);
+            bool ok = true;
+            for (int it = 0; it < n_st && ok; ++it) {
+                const int slot = it % stages, b = it & 1;
+                ok = mbar_wait_bounded(&full[slot], (it / stages) & 1, c.status);
+                // worked steps use the two ready barriers in turn (without codes: one step, the last)
+                if (ok && worked(it))
+                    ok = mbar_wait_bounded(&ready[of_q ? b : 0], of_q ? (it >> 1) & 1 : 0, c.status);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                const uint32_t a = smem_u32(of_q ? D(b) : S(slot)), h = smem_u32(H(slot));
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                    for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half)
+                            tc_mma<false>(tmem + (uint32_t)(sub * c.Rq),
+                                          umma_desc_sw128_mn(a + sub * 2 * kAtom + kk * 2048, kAtom),
+                                          umma_desc_sw128_mn(h + half * h_half + kk * 2048, kAtom), idesc,
+                                          (it | kk | half) != 0 ? 1u : 0u);
+                tc_commit(&empty[slot]);
+                if (of_q)
+                    tc_commit(&taken[b]);
+            }
+            if (!ok)
+                abort_flag = 1;
+            tc_commit(&acc_full);
+            mbar_wait_bounded(&acc_full, 0, c.status);
+        }
+        __syncwarp();
+    } else {
+        const int w = warp - 2;
+        bool ok = true;
+        if (of_q) {
+            // 64-column atom w & 3, rows 32 (w >> 2) .. +31: four chunks of 16 codes a thread; the
+            // rows of a phase (r and r + 4) meet no bank twice, loading or storing
+            const int atom = w & 3, row0 = (w >> 2) * 32 + (lane >> 3) + ((lane >> 2) & 1) * 4;
+            const int unit = (atom & 1) * 4 + (lane & 3), bunit = 2 * (lane & 3), swap = (lane >> 2) & 1;
+            const int64_t k = n0 + atom * 64;
+            const float* sc = k < p.K ? p.q_scale + (k >> p.g_shift) * c.M : nullptr;
+            float next[4];
+            auto load_scales = [&](int it) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int row = row0 + 8 * e;
+                    next[e] = it < n_st && sc && row < rows_of(it)
+                                  ? __ldg(sc + c.plan.perm[seg0 + (rank + it * z) * 64 + row])
+                                  : 0.f;
+                }
+            };
+            load_scales(0);
+            for (int it = 0; it < n_st; ++it) {
+                float s[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    s[e] = next[e];
+                load_scales(it + 1);
+                const int slot = it % stages, b = it & 1;
+                if (!mbar_wait_bounded(&full[slot], (it / stages) & 1, c.status) ||
+                    (it >= 2 && !mbar_wait_bounded(&taken[b], ((it >> 1) & 1) ^ 1, c.status)) || aborted(&abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const uint8_t* raw = S(slot) + (atom >> 1) * kAtom;
+                const uint32_t dst = smem_u32(D(b)) + atom * kAtom;
+                uint4 v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] = *reinterpret_cast<const uint4*>(raw + swz128(row0 + 8 * e, unit));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t cw[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+                    uint32_t o[8];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const uint32_t u = cw[y] ^ 0x80808080u;
+                        float fv[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)  // the byte in the mantissa of 2^23: exact
+                            fv[x] = (__uint_as_float(prmt(u, 0x4B000000u, 0x7650u + (uint32_t)x)) - 8388736.f) * s[e];
+                        o[2 * y] = pack_h16x2(fv[0], fv[1], f16);
+                        o[2 * y + 1] = pack_h16x2(fv[2], fv[3], f16);
+                    }
+                    const int row = row0 + 8 * e;
+                    const uint32_t lo = dst + swz128(row, bunit), hi = dst + swz128(row, bunit + 1);
+                    if (swap) {
+                        st_shared_v4(hi, o[4], o[5], o[6], o[7]);
+                        st_shared_v4(lo, o[0], o[1], o[2], o[3]);
+                    } else {
+                        st_shared_v4(lo, o[0], o[1], o[2], o[3]);
+                        st_shared_v4(hi, o[4], o[5], o[6], o[7]);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&ready[b]);
+            }
+        } else if (n_st > 0 && rows_of(n_st - 1) < 64) {
+            // the adapter's last step: zeros past its last token
+            const int it = n_st - 1, slot = it % stages, r0 = rows_of(it);
+            ok = mbar_wait_bounded(&full[slot], (it / stages) & 1, c.status);
             if (ok) {
-                const uint32_t s0 = smem_u32(S(slot)), h0 = smem_u32(H(slot));
-                if (!of_q) {
-                    const int64_t n = n0 + 8 * lane;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int row = warp + 8 * e, m = toks[it % 3][row];
-                        const bool in = m >= 0 && n < ncols;
-                        cp_async16(s0 + (lane >> 3) * kAtom + swz128(row, lane & 7), in ? src + (size_t)m * ncols + n : src, in);
-                    }
-                } else {
-                    const int ch = tid & 15, swap = (ch >> 2) & 1;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int row = (tid >> 4) + 16 * e;
-                        const uint32_t w[4] = {qv[e].x, qv[e].y, qv[e].z, qv[e].w};
-                        uint32_t o[8];
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            const uint32_t v = w[b] ^ 0x80808080u;
-                            float fv[4];
-#pragma unroll
-                            for (int y = 0; y < 4; ++y)  // the byte in the mantissa of 2^23: exact
-                                fv[y] = (__uint_as_float(prmt(v, 0x4B000000u, 0x7650u + (uint32_t)y)) - 8388736.f) * qs[e];
-                            o[2 * b] = pack_h16x2(fv[0], fv[1], f16);
-                            o[2 * b + 1] = pack_h16x2(fv[2], fv[3], f16);
-                        }
-                        const uint32_t at = s0 + (ch >> 2) * kAtom;
-                        const int un = 2 * (ch & 3);
-                        if (swap) {  // chunks of two atoms in a phase: other units first
-                            st_shared_v4(at + swz128(row, un + 1), o[4], o[5], o[6], o[7]);
-                            st_shared_v4(at + swz128(row, un), o[0], o[1], o[2], o[3]);
-                        } else {
-                            st_shared_v4(at + swz128(row, un), o[0], o[1], o[2], o[3]);
-                            st_shared_v4(at + swz128(row, un + 1), o[4], o[5], o[6], o[7]);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int idx = tid + 256 * e;
-                    if (idx < pieces) {
-                        const int row = idx / per, col = 4 * (idx % per);
-                        uint32_t a0, a1, b0, b1;
-                        split2<T>(hv[e].x * to, hv[e].y * to, a0, b0);
-                        split2<T>(hv[e].z * to, hv[e].w * to, a1, b1);
-                        const uint32_t at = h0 + (col >> 6) * kAtom + swz128(row, (col & 63) >> 3) + (col & 7) * 2;
-                        st_shared_v2(at, a0, a1);
-                        st_shared_v2(at + h_bytes, b0, b1);
-                    }
-                }
-                cp_async_commit();
-                if (of_q) {
-                    publish(it);
-                } else if (it >= 2) {
-                    cp_async_wait<2>();
-                    publish(it - 2);
-                }
+                const uint32_t s0 = smem_u32(S(slot));
+                for (int e = w * 32 + lane; e < (64 - r0) * 32; e += kGramWork * 32)
+                    st_shared_v4(s0 + ((e & 31) >> 3) * kAtom + (r0 + (e >> 5)) * 128 + (e & 7) * 16, 0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
             }
-            if (it + 1 < n_st)
-                load_regs(it + 1);
-            if (tid < 64)
-                toks[(it + 2) % 3][tid] = next;
-            asm volatile("bar.sync 1, 256;" ::: "memory");
+            __syncwarp();
+            if (ok && lane == 0)
+                mbar_arrive(&ready[0]);
         }
-        if (ok && !of_q) {
-            if (it >= 2) {
-                cp_async_wait<1>();
-                publish(it - 2);
-            }
-            if (it >= 1) {
-                cp_async_wait<0>();
-                publish(it - 1);
-            }
-        }
-        cp_async_wait<0>();
         if (!ok)
             abort_flag = 1;
         const bool sums = n_st > 0 && mbar_wait_bounded(&acc_full, 0, c.status) && !aborted(&abort_flag);
         tc_fence_after();
         asm volatile("bar.sync 1, 256;" ::: "memory");
-        const int pitch = c.Rq + 4, sub = warp >> 2, row = sub * 128 + 32 * (warp & 3) + lane;
-        float* red = reinterpret_cast<float*>(smem) + (size_t)row * pitch;
+        const int pitch = c.Rq + 4, sub = w >> 2, q = warp & 3;
+        float* red = reinterpret_cast<float*>(smem) + (size_t)(sub * 128 + 32 * q + lane) * pitch;
         for (int col = 0; col < c.Rq; col += 16) {
             uint32_t r[16];
             if (sums) {
-                tmem_ld16(tmem + (uint32_t)(sub * c.Rq + col) + ((uint32_t)(32 * (warp & 3)) << 16), r);
+                tmem_ld16(tmem + (uint32_t)(sub * c.Rq + col) + ((uint32_t)(32 * q) << 16), r);
             } else {
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
@@ -772,48 +1132,20 @@ __global__ void __launch_bounds__(kGramThreads) adapters_gram_kernel(const GramP
                 *reinterpret_cast<uint4*>(red + col + e) = make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
         }
         tc_fence_before();
-    } else {
-        if (lane == 0) {
-            const uint32_t ty = f16 ? 0u : (1u << 7) | (1u << 10);
-            const uint32_t idesc = (1u << 4) | ty | (1u << 15) | (1u << 16) | ((uint32_t)(c.Rq >> 3) << 17) |
-                                   ((uint32_t)(128 >> 4) << 24);
-            bool ok = true;
-            for (int it = 0; it < n_st && ok; ++it) {
-                const int slot = it % kGramStages;
-                ok = mbar_wait_bounded(&full[slot], (it / kGramStages) & 1, c.status);
-                if (!ok)
-                    break;
-                tc_fence_after();
-                const uint32_t a = smem_u32(S(slot)), b = smem_u32(H(slot));
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-                    for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-                        for (int part = 0; part < 2; ++part)
-                            tc_mma<false>(tmem + (uint32_t)(sub * c.Rq),
-                                          umma_desc_sw128_mn(a + sub * 2 * kAtom + kk * 2048, kAtom),
-                                          umma_desc_sw128_mn(b + part * h_bytes + kk * 2048, kAtom), idesc,
-                                          (it | kk | part) != 0 ? 1u : 0u);
-                tc_commit(&empty[slot]);
-            }
-            if (!ok)
-                abort_flag = 1;
-            tc_commit(&acc_full);
-            mbar_wait_bounded(&acc_full, 0, c.status);
-        }
-        __syncwarp();
     }
     __syncthreads();
     cluster_sync();
-    if (warp < 8) {
+    if (warp >= 2) {
         // CTA j adds the cluster's parts of its share of the 256 columns, in order
         const int share = 256 / z, row0 = rank * share, pitch = c.Rq + 4;
         const uint32_t mine = smem_u32(smem);
-        const float sc = of_dy ? (tokens > 0 ? p.scales[i] * back : 0.f) : back;
+        float to, back = 1.f;
+        if constexpr (f16)
+            half_scale<T>(adapter_max(c, i, of_dy ? 1 : 0, p.parts, lane), to, back);
+        const float sc = of_dy ? p.scales[i] * back : back;
         T* da = static_cast<T*>(p.da);
         T* db = static_cast<T*>(p.db);
-        for (int e = tid; e < share * c.R; e += 256) {
+        for (int e = tid - 64; e < share * c.R; e += kGramWork * 32) {
             // consecutive threads write consecutive elements: r of dB's rows, columns of dA's
             const int row = row0 + (of_dy ? e / c.R : e % share), r = of_dy ? e % c.R : e / share;
             if (n0 + row >= ncols)
@@ -829,7 +1161,7 @@ __global__ void __launch_bounds__(kGramThreads) adapters_gram_kernel(const GramP
         }
     }
     cluster_sync();
-    if (warp == 8)
+    if (warp == 1)
         tmem_dealloc(tmem, (uint32_t)p.tmem_cols);
 }
 
@@ -844,10 +1176,6 @@ bool a16(std::initializer_list<const void*> ps)
 }
 int rank_up(int64_t R) { return (int)((R + 15) / 16 * 16); }
 size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
-size_t h_bytes(int64_t M, int64_t L, int64_t R)
-{
-    return up256((size_t)max_tiles(M, L, kTileL) * kTileL * rank_up(R) * sizeof(float));
-}
 uint32_t tmem_columns(int n)
 {
     uint32_t c = 32;
@@ -856,22 +1184,43 @@ uint32_t tmem_columns(int n)
     return c;
 }
 
-Common common_of(const PlanView& plan, int64_t M, int64_t L, int64_t R, void* ws, const DeviceInfo& dev)
+// The workspace: halves for the wide product, halves of v and u for the grams, and what fp16 needs.
+struct Layout {
+    size_t halves, back, v, tile_max, total;
+    Layout(int64_t M, int64_t L, int64_t R)
+    {
+        const size_t tiles = (size_t)max_tiles(M, L, kTileL), slots = tiles * kTileL;
+        halves = up256(2 * slots * (size_t)rank_up(R) * 2);
+        back = up256(slots * sizeof(float));
+        v = up256(slots * (size_t)rank_up(R) * sizeof(float));
+        tile_max = up256(tiles * kMaxSplit * 2 * sizeof(float));
+        total = 3 * halves + back + v + tile_max;
+    }
+};
+
+Common common_of(const PlanView& plan, qlin_dtype dt, int64_t M, int64_t L, int64_t R, void* ws, const DeviceInfo& dev)
 {
+    const Layout l(M, L, R);
+    uint8_t* p = static_cast<uint8_t*>(ws);
     Common c;
     c.plan = plan;
     c.M = M;
+    c.slots = max_tiles(M, L, kTileL) * kTileL;
     c.L = (int)L;
     c.R = (int)R;
     c.Rq = rank_up(R);
-    c.h = static_cast<float*>(ws);
-    c.tile_max = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + h_bytes(M, L, R));
+    c.row_halves = reinterpret_cast<uint16_t*>(p);
+    c.v_halves = dt == QLIN_F16 ? reinterpret_cast<uint16_t*>(p + l.halves) : c.row_halves;
+    c.u_halves = reinterpret_cast<uint16_t*>(p + 2 * l.halves);
+    c.row_back = reinterpret_cast<float*>(p + 3 * l.halves);
+    c.v = reinterpret_cast<float*>(p + 3 * l.halves + l.back);
+    c.tile_max = reinterpret_cast<float*>(p + 3 * l.halves + l.back + l.v);
     c.status = dev.status;
     return c;
 }
 
 // A launch behind the stream's previous kernel (the kernels wait for it before touching memory),
-// with clusters of cluster_x CTAs along x.
+// with clusters of cluster_x CTAs along x (0: none).
 template <typename P>
 cudaError_t launch(void (*kern)(const P), dim3 grid, int threads, int smem, int cluster_x, const P& prm, cudaStream_t st)
 {
@@ -900,6 +1249,20 @@ cudaError_t launch(void (*kern)(const P), dim3 grid, int threads, int smem, int 
 template <typename T>
 CUtensorMapDataType tm_type() { return Is16<T>::f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16; }
 
+// Token rows [M][cols]: boxes of 64 rows, and single rows, 128 bytes wide.
+bool row_maps(RowMaps& m, CUtensorMapDataType dt, int elem, const void* p, int64_t M, int64_t cols)
+{
+    const uint32_t w = 128 / elem;
+    return encode_tmap_2d(&m.box, dt, p, (uint64_t)cols, (uint64_t)M, (uint64_t)cols * elem, w, 64) &&
+           encode_tmap_2d(&m.row, dt, p, (uint64_t)cols, (uint64_t)M, (uint64_t)cols * elem, w, 1);
+}
+// Halves [2 slots][Rq] in boxes of 64 ranks.
+template <typename T>
+bool half_map(CUtensorMap& m, const Common& c, const uint16_t* p, uint32_t rows)
+{
+    return encode_tmap_2d(&m, tm_type<T>(), p, (uint64_t)c.Rq, (uint64_t)(2 * c.slots), (uint64_t)c.Rq * 2, 64, rows);
+}
+
 // CTAs that share a contraction of K: more until two an SM have work, at least four steps each.
 int narrow_split(const Common& c, int64_t K, const DeviceInfo& dev)
 {
@@ -916,27 +1279,25 @@ cudaError_t launch_narrow(const Common& c, const void* w, int64_t K, const void*
 {
     NarrowParams p;
     p.c = c;
-    p.w = w;
     p.K = K;
     p.scales = scales;
     p.u_in = u_in;
     p.u_out = u_out;
     // a factor of box rows: forward Rq rows of 64 k; backward 64 rows of 64 ranks, an atom each
-    if (!(FWD ? encode_tmap_3d(&p.tm_f, tm_type<T>(), f, (uint64_t)K, (uint64_t)c.R, (uint64_t)c.L, 2, 64, (uint32_t)c.Rq)
+    if (!row_maps(p.w, tm_type<T>(), 2, w, c.M, K) ||
+        !(FWD ? encode_tmap_3d(&p.tm_f, tm_type<T>(), f, (uint64_t)K, (uint64_t)c.R, (uint64_t)c.L, 2, 64, (uint32_t)c.Rq)
               : encode_tmap_3d(&p.tm_f, tm_type<T>(), f, (uint64_t)c.R, (uint64_t)K, (uint64_t)c.L, 2, 64, 64)))
         return cudaErrorInvalidValue;
     p.f_bytes = FWD ? c.Rq * 128 : (c.Rq + 63) / 64 * (int)kAtom;
     const int stage = 2 * (int)kAtom + p.f_bytes;
     p.stages = 110 * 1024 / stage < kNarrowMaxStages ? 110 * 1024 / stage : kNarrowMaxStages;
-    if (p.stages < 4)
-        p.stages = 4;
     const int red = 128 * (c.Rq + 4) * 4;
     const int smem = (p.stages * stage > red ? p.stages * stage : red) + 1024;
     p.tmem_cols = (int)tmem_columns(c.Rq);
-    const int64_t tiles = max_tiles(c.M, c.L, kTileL);
     const int z = narrow_split(c, K, dev);
     p.steps = (int)((K + 63) / 64 + z - 1) / z;
-    return launch(adapters_narrow_tc_kernel<T, FWD>, dim3((unsigned)z, (unsigned)tiles), kNarrowThreads, smem, z, p, st);
+    const dim3 grid((unsigned)z, (unsigned)max_tiles(c.M, c.L, kTileL));
+    return launch(adapters_narrow_kernel<T, FWD>, grid, kNarrowThreads, smem, z, p, st);
 }
 
 template <typename T, bool FWD>
@@ -945,26 +1306,25 @@ cudaError_t launch_wide(const Common& c, const void* f, const float* scales, con
 {
     WideParams p;
     p.c = c;
-    p.f = f;
     p.scales = scales;
-    p.base = base;
+    p.base_p = base;
     p.out = out;
     p.N = N;
+    if (!row_maps(p.base, tm_type<T>(), 2, base ? base : out, c.M, N) || !half_map<T>(p.tm_h, c, c.row_halves, 128) ||
+        !(FWD ? encode_tmap_3d(&p.tm_f, tm_type<T>(), f, (uint64_t)c.R, (uint64_t)N, (uint64_t)c.L, 2, 64, kWideCols)
+              : encode_tmap_3d(&p.tm_f, tm_type<T>(), f, (uint64_t)N, (uint64_t)c.R, (uint64_t)c.L, 2, 64, (uint32_t)c.Rq)))
+        return cudaErrorInvalidValue;
+    const int atoms = (c.Rq + 63) / 64, h = 2 * atoms * 2 * (int)kAtom;
+    p.f_bytes = FWD ? atoms * 2 * (int)kAtom : 2 * c.Rq * 128;
+    const int stage = 4 * (int)kAtom + p.f_bytes, room = 224 * 1024 - h;
+    p.stages = room / stage < kWideMaxStages ? room / stage : kWideMaxStages;
     const int64_t tiles = max_tiles(c.M, c.L, kTileL);
-    // strips of 2048 columns, shorter while that leaves fewer than four CTAs an SM
-    p.strip = 2048;
-    while (p.strip > 128 && tiles * ((N + p.strip - 1) / p.strip) < 4 * dev.sm_count)
+    // strips of 4096 columns, shorter while that leaves fewer than two CTAs an SM
+    p.strip = 4096;
+    while (p.strip > kWideCols && tiles * ((N + p.strip - 1) / p.strip) < 2 * dev.sm_count)
         p.strip /= 2;
     const dim3 grid((unsigned)((N + p.strip - 1) / p.strip), (unsigned)tiles);
-    const int kt = c.Rq / 16;
-    constexpr int th = kWideWarps * 32;
-    if (kt <= 1)
-        return launch(adapters_wide_tc_kernel<T, FWD, 1, 2>, grid, th, 0, 0, p, st);
-    if (kt <= 2)
-        return launch(adapters_wide_tc_kernel<T, FWD, 2, 2>, grid, th, 0, 0, p, st);
-    if (kt <= 4)
-        return launch(adapters_wide_tc_kernel<T, FWD, 4, 2>, grid, th, 0, 0, p, st);
-    return launch(adapters_wide_tc_kernel<T, FWD, 8, 1>, grid, th, 0, 0, p, st);
+    return launch(adapters_wide_kernel<T, FWD>, grid, kWideThreads, h + p.stages * stage + 1024, 0, p, st);
 }
 
 template <typename T>
@@ -972,12 +1332,8 @@ cudaError_t launch_grams(const Common& c, const AdapterBwdArgs& a, cudaStream_t 
 {
     GramParams p;
     p.c = c;
-    p.dy = a.dy;
-    p.u = a.u;
     p.scales = a.scales;
-    p.x = a.x;
-    p.q = a.q;
-    p.q_scale = a.q_scale;
+    p.q_scale = a.q ? a.q_scale : nullptr;
     p.g_shift = a.g == 64 ? 6 : a.g == 128 ? 7 : 8;
     p.N = a.N;
     p.K = a.K;
@@ -987,20 +1343,54 @@ cudaError_t launch_grams(const Common& c, const AdapterBwdArgs& a, cudaStream_t 
     p.db = a.db;
     p.parts = narrow_split(c, a.N, dev);
     p.tmem_cols = (int)tmem_columns(2 * c.Rq);
-    const int ring = kGramStages * (4 * (int)kAtom + 2 * ((c.Rq + 63) / 64) * (int)kAtom), red = 256 * (c.Rq + 4) * 4;
-    const int smem = (ring > red ? ring : red) + 1024;
+    if (!row_maps(p.dy, tm_type<T>(), 2, a.dy, c.M, a.N) ||
+        !(a.q ? row_maps(p.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.q, c.M, a.K)
+              : row_maps(p.x, tm_type<T>(), 2, a.x, c.M, a.K)) ||
+        !half_map<T>(p.tm_u, c, c.u_halves, 64) || !half_map<T>(p.tm_v, c, c.v_halves, 64))
+        return cudaErrorInvalidValue;
+    p.room = 224 * 1024;
     const int64_t jobs = (int64_t)c.L * (p.strips_y + p.strips_x);
     // split an adapter's tokens until every SM has work, at least two steps each on average
     int z = 1;
     while (z < kMaxSplit && jobs * z < dev.sm_count && c.M / c.L / 64 >= 4 * z)
         z *= 2;
-    return launch(adapters_gram_kernel<T>, dim3((unsigned)z, (unsigned)jobs), kGramThreads, smem, z, p, st);
+    return launch(adapters_gram_kernel<T>, dim3((unsigned)z, (unsigned)jobs), kGramThreads, p.room + 1024, z, p, st);
+}
+
+template <typename T>
+cudaError_t launch_decode(const Common& c, const AdapterFwdArgs& a, cudaStream_t st)
+{
+    DecodeParams p;
+    p.c = c;
+    p.x = a.x;
+    p.a = a.a;
+    p.b = a.b;
+    p.scales = a.scales;
+    p.base = a.base;
+    p.out = a.out;
+    p.u = a.u;
+    p.K = a.K;
+    p.N = a.N;
+    const int z = 8;
+    const dim3 grid((unsigned)z, (unsigned)max_tiles(a.M, a.L, kTileS));
+    auto smem = [&](int kt) { return ((kDecodeWarps + z) * 16 * kt * 8 + 8 * (16 * kt + 4)) * (int)sizeof(float); };
+    const int kt = c.Rq / 16;
+    constexpr int th = kDecodeWarps * 32;
+    if (kt <= 1)
+        return launch(adapters_decode_kernel<T, 1>, grid, th, smem(1), z, p, st);
+    if (kt <= 2)
+        return launch(adapters_decode_kernel<T, 2>, grid, th, smem(2), z, p, st);
+    if (kt <= 4)
+        return launch(adapters_decode_kernel<T, 4>, grid, th, smem(4), z, p, st);
+    return launch(adapters_decode_kernel<T, 8>, grid, th, smem(8), z, p, st);
 }
 
 template <typename T>
 cudaError_t forward_t(const AdapterFwdArgs& a, cudaStream_t st, const DeviceInfo& dev)
 {
-    const Common c = common_of(a.plan, a.M, a.L, a.R, a.ws, dev);
+    const Common c = common_of(a.plan, a.dt, a.M, a.L, a.R, a.ws, dev);
+    if (getenv("QDEC") ? a.M <= atoi(getenv("QDEC")) : a.M <= 128)
+        return launch_decode<T>(c, a, st);
     const cudaError_t e = launch_narrow<T, true>(c, a.x, a.K, a.a, nullptr, nullptr, a.u, st, dev);
     return e != cudaSuccess ? e : launch_wide<T, true>(c, a.b, a.scales, a.base, a.out, a.N, st, dev);
 }
@@ -1008,8 +1398,12 @@ cudaError_t forward_t(const AdapterFwdArgs& a, cudaStream_t st, const DeviceInfo
 template <typename T>
 cudaError_t backward_t(const AdapterBwdArgs& a, cudaStream_t st, const DeviceInfo& dev)
 {
-    const Common c = common_of(a.plan, a.M, a.L, a.R, a.ws, dev);
+    const Common c = common_of(a.plan, a.dt, a.M, a.L, a.R, a.ws, dev);
     cudaError_t e = launch_narrow<T, false>(c, a.dy, a.N, a.b, a.scales, a.u, nullptr, st, dev);
+    if (e == cudaSuccess && Is16<T>::f16) {
+        const SplitParams p = {c, a.u, narrow_split(c, a.N, dev)};
+        e = launch(adapters_split_kernel, dim3((unsigned)max_tiles(a.M, a.L, kTileL)), 256, 0, 0, p, st);
+    }
     if (e == cudaSuccess)
         e = launch_grams<T>(c, a, st, dev);
     if (e == cudaSuccess && a.dx)
@@ -1036,10 +1430,7 @@ bool adapters_tc_takes(const AdapterBwdArgs& a)
            a16({a.dy, a.a, a.b, a.u, a.x, a.q, a.dx_base, a.dx, a.da, a.db});
 }
 
-size_t adapters_tc_workspace(int64_t M, int64_t L, int64_t R)
-{
-    return h_bytes(M, L, R) + up256((size_t)max_tiles(M, L, kTileL) * kMaxSplit * 2 * sizeof(float));
-}
+size_t adapters_tc_workspace(int64_t M, int64_t L, int64_t R) { return Layout(M, L, R).total; }
 
 cudaError_t launch_adapters_forward_tc(const AdapterFwdArgs& a, cudaStream_t st, const DeviceInfo& dev)
 {
