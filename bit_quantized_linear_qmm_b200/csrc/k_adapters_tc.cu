@@ -10,8 +10,8 @@
 // tensor cores and the threads only have to keep up.  Tokens are taken in tiles of 128 of one
 // adapter (the plan's list).  A tile whose tokens are consecutive is read in tensor-map boxes of 64
 // rows, any other by tile::gather4, four rows an instruction: no thread touches the data before
-// the tensor cores (threads with cp.async, 8 copies each a stage, reached 2.2 TB/s; boxes of the
-// same stages are bounded by memory).
+// the tensor cores.  A warp issues one gather in about 86 cycles (its lanes take turns), so four
+// warps share a stage's gathers: one warp alone loaded a gathered tile at half the speed of boxes.
 //
 // h, u and v enter their second product as two 16-bit halves, hi = round(h) and lo = round(h - hi):
 // 2^-16 of the value at most, and two MMAs instead of one.  They are kept in slots, [tile][128][Rq]
@@ -50,14 +50,13 @@ QLIN_DEV float4 ld_peer_v4(uint32_t addr)
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
+                 : "r"(addr));
     return v;
 }
 QLIN_DEV float ld_peer(uint32_t addr)
 {
     float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
     return v;
 }
 QLIN_DEV void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
@@ -129,31 +128,25 @@ struct RowMaps {
     CUtensorMap box, row;
 };
 
-// One warp: `64 n64` rows of 64 elements from column c0 (128 bytes of column for bytes), from row
-// `first`, or, where first < 0, rows `r` of each lane (lane l: rows 4 l .. of the block).
-QLIN_DEV void load_rows(uint32_t dst, const RowMaps& m, int c0, int first, const int4& r, int n64, int lane, uint64_t* bar)
+// One thread: 64 n64 rows from row `first`, 128 bytes of each from column c0.
+QLIN_DEV void load_box(uint32_t dst, const RowMaps& m, int c0, int first, int n64, uint64_t* bar)
 {
-    if (first >= 0) {
-        if (lane == 0)
-            for (int h = 0; h < n64; ++h)
-                asm volatile(
-                    "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-                    "[%1, {%2, %3}], [%4];" ::"r"(dst + h * kAtom),
-                    "l"(reinterpret_cast<uint64_t>(&m.box)), "r"(c0), "r"(first + 64 * h), "r"(smem_u32(bar))
-                    : "memory");
-    } else if (lane < 16 * n64) {
-        tma_gather4(dst + lane * 512, &m.row, c0, r, bar);
-    }
+    for (int h = 0; h < n64; ++h)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+            "[%4];" ::"r"(dst + h * kAtom),
+            "l"(reinterpret_cast<uint64_t>(&m.box)), "r"(c0), "r"(first + 64 * h), "r"(smem_u32(bar))
+            : "memory");
 }
 
-// Tokens of rows 4 lane .. 4 lane + 3 of positions [start, start + count); past the end the first
-// (its row is read and never used, or zeroed).
-QLIN_DEV int4 row_tokens(const PlanView& v, int start, int count, int lane)
+// Tokens of rows 4 i .. 4 i + 3 of positions [start, start + count); past the end the first one (its
+// row is read and never used, or zeroed).
+QLIN_DEV int4 row_tokens(const PlanView& v, int start, int count, int i)
 {
     int t[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-        t[e] = v.perm[start + (4 * lane + e < count ? 4 * lane + e : 0)];
+        t[e] = v.perm[start + (4 * i + e < count ? 4 * i + e : 0)];
     return make_int4(t[0], t[1], t[2], t[3]);
 }
 
@@ -163,12 +156,13 @@ QLIN_DEV int4 row_tokens(const PlanView& v, int start, int count, int lane)
 // [128][Rq] in tensor memory over its steps of 64; the partial sums meet through distributed shared
 // memory, CTA j adding the parts of rows 128 j / z .. in order, so h is written once and the order
 // of every sum is fixed.
-//   warp 0       the loads: activation rows, and the factor -- forward A_i [Rq rows][64 k], K-major;
-//                backward B_i [64 n][R], MN-major -- from a 3-D map, so that rows and columns past
-//                the adapter's own are zeros
-//   warp 1       tensor memory, the MMAs (M = 128, N = Rq, K = 16)
-//   warps 2..5   the epilogue
-constexpr int kNarrowThreads = 192;
+//   warps 0..3   the loads: activation rows, and (warp 0) the factor -- forward A_i [Rq rows][64 k],
+//                K-major; backward B_i [64 n][R], MN-major -- from a 3-D map, so that rows and
+//                columns past the adapter's own are zeros
+//   warp 4       tensor memory, the MMAs (M = 128, N = Rq, K = 16)
+//   warps 5..8   the epilogue
+constexpr int kLoadWarps = 4;
+constexpr int kNarrowThreads = (kLoadWarps + 1 + 4) * 32;
 constexpr int kNarrowMaxStages = 8;
 
 struct NarrowParams {
@@ -221,7 +215,7 @@ __global__ void __launch_bounds__(kNarrowThreads) adapters_narrow_kernel(const _
                     p.u_out[(size_t)c.plan.perm[d.start + row0 + i / c.R] * c.R + i % c.R] = 0.f;
         return;
     }
-    if (warp == 1)
+    if (warp == kLoadWarps)
         tmem_alloc(&tmem_s, (uint32_t)p.tmem_cols);
     tc_fence_before();
     __syncthreads();
@@ -236,10 +230,12 @@ __global__ void __launch_bounds__(kNarrowThreads) adapters_narrow_kernel(const _
     auto F = [&](int s) { return smem + s * stage_bytes + 2 * kAtom; };
     const int pitch = c.Rq + 4;  // floats: an odd number of 16-byte units, so rows meet all banks
 
-    if (warp == 0) {
-        const int4 tok = d.first >= 0 ? make_int4(0, 0, 0, 0) : row_tokens(c.plan, d.start, d.count, lane);
+    if (warp < kLoadWarps) {
+        const int piece = 8 * warp + lane;  // lanes 0..7: four rows each of a gathered tile
+        const bool box = d.first >= 0;
+        const int4 tok = box || lane >= 8 ? make_int4(0, 0, 0, 0) : row_tokens(c.plan, d.start, d.count, piece);
         int it = 0;
-        for (; it < n_st; ++it) {
+        for (; it < n_st && (!box || warp == 0); ++it) {
             const int slot = it % p.stages;
             const bool ok = it < p.stages || mbar_wait_bounded(&empty[slot], ((it / p.stages) & 1) ^ 1, c.status);
             if (__any_sync(0xffffffffu, !ok || aborted(&abort_flag))) {
@@ -247,7 +243,7 @@ __global__ void __launch_bounds__(kNarrowThreads) adapters_narrow_kernel(const _
                 break;
             }
             const int k = (k_first + it) * 64;
-            if (lane == 0) {
+            if (tid == 0) {
                 mbar_arrive_expect_tx(&full[slot], (unsigned)stage_bytes);
                 if constexpr (FWD) {
                     tma_load_3d(F(slot), &p.tm_f, k, 0, d.adapter, &full[slot]);
@@ -255,13 +251,16 @@ __global__ void __launch_bounds__(kNarrowThreads) adapters_narrow_kernel(const _
                     for (int a = 0; a * 64 < c.Rq; ++a)
                         tma_load_3d(F(slot) + a * kAtom, &p.tm_f, a * 64, k, d.adapter, &full[slot]);
                 }
+                if (box)
+                    load_box(smem_u32(X(slot)), p.w, k, d.first, 2, &full[slot]);
             }
             __syncwarp();
-            load_rows(smem_u32(X(slot)), p.w, k, d.first, tok, 2, lane, &full[slot]);
+            if (!box && lane < 8)
+                tma_gather4(smem_u32(X(slot)) + piece * 512, &p.w.row, k, tok, &full[slot]);
         }
         for (int j = it - p.stages < 0 ? 0 : it - p.stages; j < it; ++j)  // no copy may land after the exit
             mbar_wait_bounded(&full[j % p.stages], (j / p.stages) & 1, c.status);
-    } else if (warp == 1) {
+    } else if (warp == kLoadWarps) {
         if (lane == 0) {
             const uint32_t ty = f16 ? 0u : (1u << 7) | (1u << 10);
             const uint32_t idesc = (1u << 4) | ty | (FWD ? 0u : 1u << 16) | ((uint32_t)(c.Rq >> 3) << 17) |
@@ -310,27 +309,34 @@ __global__ void __launch_bounds__(kNarrowThreads) adapters_narrow_kernel(const _
     }
     __syncthreads();
     cluster_sync();
-    if (warp >= 2) {
-        // a warp a row: lane l adds the parts of columns 4 l .. 4 l + 3
+    if (warp > kLoadWarps) {
+        // a power of two of lanes takes a row, four columns a lane: 32 / lanes rows a warp at a time
         const float sc = FWD ? 1.f : p.scales[d.adapter];
         const uint32_t mine = smem_u32(smem);
-        const int col = 4 * lane;
+        const int lanes = c.Rq <= 16 ? 4 : c.Rq <= 32 ? 8 : c.Rq <= 64 ? 16 : 32, at_once = 4 * (32 / lanes);
+        const int col = 4 * (lane & (lanes - 1));
         const size_t lo_at = (size_t)c.slots * c.Rq;
         float vmax = 0.f, umax = 0.f;
-        for (int row = row0 + warp - 2; row < row0 + rows; row += 4) {
-            const bool in = row < d.count && col < c.R;
+        for (int r0 = 0; r0 < rows; r0 += at_once) {
+            const int row = row0 + r0 + (warp - kLoadWarps - 1) * (32 / lanes) + lane / lanes;
+            const bool mine_ok = row < row0 + rows, in = mine_ok && row < d.count && col < c.R;
             const size_t at = ((size_t)t * kTileL + row) * c.Rq + col;
             const size_t tok = in ? (size_t)c.plan.perm[d.start + row] : 0;
             float4 s = make_float4(0.f, 0.f, 0.f, 0.f), u = s;
-            if (in && !FWD)
-                u = __ldg(reinterpret_cast<const float4*>(p.u_in + tok * c.R + col));
             if (in) {
-                for (int j = 0; j < z; ++j) {
-                    const float4 v = ld_peer_v4(peer_smem(mine + (uint32_t)(row * pitch + col) * 4u, (uint32_t)j));
-                    s.x += v.x;
-                    s.y += v.y;
-                    s.z += v.z;
-                    s.w += v.w;
+                const uint32_t from = mine + (uint32_t)(row * pitch + col) * 4u;
+                float4 v[kMaxSplit];
+#pragma unroll
+                for (int j = 0; j < kMaxSplit; ++j)
+                    v[j] = j < z ? ld_peer_v4(peer_smem(from, (uint32_t)j)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                if (!FWD)
+                    u = __ldg(reinterpret_cast<const float4*>(p.u_in + tok * c.R + col));
+#pragma unroll
+                for (int j = 0; j < kMaxSplit; ++j) {
+                    s.x += v[j].x;
+                    s.y += v[j].y;
+                    s.z += v[j].z;
+                    s.w += v[j].w;
                 }
                 s = make_float4(sc * s.x, sc * s.y, sc * s.z, sc * s.w);
                 if (FWD && p.u_out)
@@ -341,14 +347,13 @@ __global__ void __launch_bounds__(kNarrowThreads) adapters_narrow_kernel(const _
                 float top = fmaxf(fmaxf(finite_abs(s.x), finite_abs(s.y)), fmaxf(finite_abs(s.z), finite_abs(s.w)));
                 vmax = fmaxf(vmax, top);
                 umax = fmaxf(umax, fmaxf(fmaxf(finite_abs(u.x), finite_abs(u.y)), fmaxf(finite_abs(u.z), finite_abs(u.w))));
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1)
+                for (int o = lanes >> 1; o > 0; o >>= 1)
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                 half_scale<T>(top, to, back);
-                if (lane == 0)
+                if (col == 0 && mine_ok)
                     c.row_back[(size_t)t * kTileL + row] = back;
             }
-            if (col < c.Rq) {
+            if (mine_ok && col < c.Rq) {
                 uint2 hi, lo;
                 split2<T>(s.x * to, s.y * to, hi.x, lo.x);
                 split2<T>(s.z * to, s.w * to, hi.y, lo.y);
@@ -371,18 +376,19 @@ __global__ void __launch_bounds__(kNarrowThreads) adapters_narrow_kernel(const _
                 umax = fmaxf(umax, __shfl_xor_sync(0xffffffffu, umax, o));
             }
             if (lane == 0) {
-                warp_max[0][warp - 2] = vmax;
-                warp_max[1][warp - 2] = umax;
+                warp_max[0][warp - kLoadWarps - 1] = vmax;
+                warp_max[1][warp - kLoadWarps - 1] = umax;
             }
             asm volatile("bar.sync 1, 128;" ::: "memory");
-            if (tid - 64 < 2) {
-                const float* w = warp_max[tid - 64];
-                c.tile_max[((size_t)t * kMaxSplit + rank) * 2 + tid - 64] = fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3]));
+            const int which = tid - (kLoadWarps + 1) * 32;
+            if (which < 2) {
+                const float* w = warp_max[which];
+                c.tile_max[((size_t)t * kMaxSplit + rank) * 2 + which] = fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3]));
             }
         }
     }
     cluster_sync();  // no CTA's shared memory goes while another reads it
-    if (warp == 1)
+    if (warp == kLoadWarps)
         tmem_dealloc(tmem, (uint32_t)p.tmem_cols);
 }
 
@@ -441,13 +447,13 @@ __global__ void __launch_bounds__(256) adapters_split_kernel(const SplitParams p
 // ------------------------------------------------------------------------------------ wide
 
 // out = base + h F: a CTA for each tile and strip of columns, 128 columns at a time.
-//   warp 0       the loads: once the halves of h; each block's factor -- forward B_i [128 n][R],
+//   warps 0..3   the loads: once the halves of h; each block's factor -- forward B_i [128 n][R],
 //                K-major; backward A_i [Rq r][128 k], MN-major -- and base [128 rows][128 columns]
-//   warp 1       two accumulators of 128 columns; hi and lo halves on the same factor block
-//   warps 2..9   32 rows by 64 columns each: the sum, scaled, onto base in shared memory, then out in
+//   warp 4       two accumulators of 128 columns; hi and lo halves on the same factor block
+//   warps 5..12  32 rows by 64 columns each: the sum, scaled, onto base in shared memory, then out in
 //                whole 128-byte pieces of a row (base's own place serves as the staging buffer)
 constexpr int kWideEpi = 8;
-constexpr int kWideThreads = (2 + kWideEpi) * 32;
+constexpr int kWideThreads = (kLoadWarps + 1 + kWideEpi) * 32;
 constexpr int kWideMaxStages = 4;
 constexpr int kWideCols = 128;
 
@@ -507,7 +513,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapters_wide_kernel(const __
         }
         return;
     }
-    if (warp == 1)
+    if (warp == kLoadWarps)
         tmem_alloc(&tmem_s, 2 * kWideCols);
     tc_fence_before();
     __syncthreads();
@@ -522,16 +528,18 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapters_wide_kernel(const __
     auto B = [&](int s) { return smem + 2 * h_half + s * stage_bytes; };
     auto F = [&](int s) { return smem + 2 * h_half + s * stage_bytes + base_bytes; };
 
-    if (warp == 0) {
-        const int4 tok = d.first >= 0 ? make_int4(0, 0, 0, 0) : row_tokens(c.plan, d.start, d.count, lane);
-        if (lane == 0) {
+    if (warp < kLoadWarps) {
+        const int piece = 16 * (warp & 1) + lane;  // lanes 0..15: four rows each of a gathered 64-column half
+        const bool box = d.first >= 0;
+        const int4 tok = box || lane >= 16 ? make_int4(0, 0, 0, 0) : row_tokens(c.plan, d.start, d.count, piece);
+        if (tid == 0) {
             mbar_arrive_expect_tx(&h_full, 2u * (unsigned)h_half);
             for (int half = 0; half < 2; ++half)
                 for (int a = 0; a < atoms; ++a)
                     tma_load_2d(Hs + half * h_half + a * 2 * kAtom, &p.tm_h, a * 64, (int)(half * c.slots) + t * kTileL, &h_full);
         }
         int it = 0;
-        for (; it < blocks; ++it) {
+        for (; it < blocks && (warp == 0 || (!box && p.base_p)); ++it) {
             const int slot = it % p.stages;
             const bool ok = it < p.stages || mbar_wait_bounded(&empty[slot], ((it / p.stages) & 1) ^ 1, c.status);
             if (__any_sync(0xffffffffu, !ok || aborted(&abort_flag))) {
@@ -539,7 +547,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapters_wide_kernel(const __
                 break;
             }
             const int n = (int)n_begin + it * kWideCols;
-            if (lane == 0) {
+            if (tid == 0) {
                 mbar_arrive_expect_tx(&full[slot], (unsigned)(p.f_bytes + (p.base_p ? base_bytes : 0)));
                 if constexpr (FWD) {
                     for (int a = 0; a < atoms; ++a)
@@ -548,16 +556,20 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapters_wide_kernel(const __
                     for (int a = 0; a < 2; ++a)
                         tma_load_3d(F(slot) + a * c.Rq * 128, &p.tm_f, n + a * 64, 0, d.adapter, &full[slot]);
                 }
+                if (box && p.base_p)
+                    for (int a = 0; a < 2; ++a)
+                        load_box(smem_u32(B(slot)) + a * 2 * kAtom, p.base, n + a * 64, d.first, 2, &full[slot]);
             }
             __syncwarp();
-            if (p.base_p)
-                for (int a = 0; a < 2; ++a)
-                    load_rows(smem_u32(B(slot)) + a * 2 * kAtom, p.base, n + a * 64, d.first, tok, 2, lane, &full[slot]);
+            if (!box && p.base_p && lane < 16) {
+                const int a = warp >> 1;
+                tma_gather4(smem_u32(B(slot)) + a * 2 * kAtom + piece * 512, &p.base.row, n + a * 64, tok, &full[slot]);
+            }
         }
         mbar_wait_bounded(&h_full, 0, c.status);
         for (int j = it - p.stages < 0 ? 0 : it - p.stages; j < it; ++j)
             mbar_wait_bounded(&full[j % p.stages], (j / p.stages) & 1, c.status);
-    } else if (warp == 1) {
+    } else if (warp == kLoadWarps) {
         if (lane == 0) {
             const uint32_t ty = f16 ? 0u : (1u << 7) | (1u << 10);
             const uint32_t idesc = (1u << 4) | ty | (FWD ? 0u : 1u << 16) | ((uint32_t)(kWideCols >> 3) << 17) |
@@ -592,7 +604,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapters_wide_kernel(const __
         }
         __syncwarp();
     } else {
-        const int q = warp & 3, half = (warp - 2) >> 2, row = 32 * q + lane;
+        const int q = warp & 3, half = (warp - kLoadWarps - 1) >> 2, row = 32 * q + lane;
         const int my_tok = row < d.count ? c.plan.perm[d.start + row] : -1;
         float rs = FWD ? p.scales[d.adapter] : 1.f;
         if constexpr (f16)
@@ -647,7 +659,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapters_wide_kernel(const __
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 1)
+    if (warp == kLoadWarps)
         tmem_dealloc(tmem, 2 * kWideCols);
 }
 
@@ -884,13 +896,13 @@ __global__ void __launch_bounds__(kDecodeWarps * 32) adapters_decode_kernel(cons
 // adapter's tokens, 64 at a time, the steps dealt round the cluster's CTAs.  S (dy, x or the
 // restored x) and H (the halves of u or v) lie token by token in shared memory, which is MN-major
 // for both operands; nothing is transposed.
-//   warp 0       the loads: S in 64-column boxes or gathers (codes: 128-byte ones), H in 64-rank boxes
-//   warp 1       tensor memory, the MMAs (two of M = 128 for hi and for lo, N = Rq, K = 16)
-//   warps 2..9   codes: s q in fp32, rounded once to the operand type, into a ring of two buffers;
+//   warps 0..3   the loads: S in 64-column boxes or gathers (codes: 128-byte ones), H in 64-rank boxes
+//   warp 4       tensor memory, the MMAs (two of M = 128 for hi and for lo, N = Rq, K = 16)
+//   warps 5..12  codes: s q in fp32, rounded once to the operand type, into a ring of two buffers;
 //                rows past the adapter's last token: zeros (only there, so what another adapter's
 //                row holds enters no sum); then the epilogue
 constexpr int kGramWork = 8;
-constexpr int kGramThreads = (2 + kGramWork) * 32;
+constexpr int kGramThreads = (kLoadWarps + 1 + kGramWork) * 32;
 constexpr int kGramMaxStages = 6;
 
 struct GramParams {
@@ -933,7 +945,7 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
         abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 1)
+    if (warp == kLoadWarps)
         tmem_alloc(&tmem_s, (uint32_t)p.tmem_cols);
     tc_fence_before();
     __syncthreads();
@@ -960,40 +972,38 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
     // a step waits for the worker warps where there is something to decode or to clear
     auto worked = [&](int it) { return of_q || rows_of(it) < 64; };
 
-    if (warp == 0) {
+    if (warp < kLoadWarps) {
         const RowMaps& m = of_dy ? p.dy : p.x;
+        const int width = of_q ? 128 : 64, blocks = src_bytes / (int)kAtom;  // 128-byte columns: a warp each
         int it = 0;
         for (; it < n_st; ++it) {
             const int slot = it % stages, step = rank + it * z;
             const AdapterTile d = c.plan.tiles_l[tile0 + (step >> 1)];
-            const int first = d.first >= 0 ? d.first + (step & 1) * 64 : -1;
             const int4 tok = row_tokens(c.plan, seg0 + step * 64, rows_of(it), lane & 15);
             const bool ok = it < stages || mbar_wait_bounded(&empty[slot], ((it / stages) & 1) ^ 1, c.status);
             if (__any_sync(0xffffffffu, !ok || aborted(&abort_flag))) {
                 abort_flag = 1;
                 break;
             }
-            if (lane == 0) {
+            const uint32_t s0 = smem_u32(S(slot));
+            if (tid == 0) {
                 mbar_arrive_expect_tx(&full[slot], (unsigned)stage_bytes);
                 const int slot0 = (tile0 + (step >> 1)) * kTileL + (step & 1) * 64;
                 for (int half = 0; half < 2; ++half)
                     for (int a = 0; a * 64 < c.Rq; ++a)
                         tma_load_2d(H(slot) + half * h_half + a * kAtom, of_dy ? &p.tm_u : &p.tm_v, a * 64,
                                     (int)(half * c.slots) + slot0, &full[slot]);
+                if (d.first >= 0)
+                    for (int a = 0; a < blocks; ++a)
+                        load_box(s0 + a * kAtom, m, (int)n0 + a * width, d.first + (step & 1) * 64, 1, &full[slot]);
             }
             __syncwarp();
-            const uint32_t s0 = smem_u32(S(slot));
-            if (first >= 0) {
-                for (int a = 0; a * (int)kAtom < src_bytes; ++a)
-                    load_rows(s0 + a * kAtom, m, (int)n0 + a * (of_q ? 128 : 64), first, tok, 1, lane, &full[slot]);
-            } else {  // two blocks of 64 rows at a time, a half of the warp each
-                for (int a = lane >> 4; a * (int)kAtom < src_bytes; a += 2)
-                    tma_gather4(s0 + a * kAtom + (lane & 15) * 512, &m.row, (int)n0 + a * (of_q ? 128 : 64), tok, &full[slot]);
-            }
+            if (d.first < 0 && warp < blocks && lane < 16)
+                tma_gather4(s0 + warp * kAtom + lane * 512, &m.row, (int)n0 + warp * width, tok, &full[slot]);
         }
         for (int j = it - stages < 0 ? 0 : it - stages; j < it; ++j)
             mbar_wait_bounded(&full[j % stages], (j / stages) & 1, c.status);
-    } else if (warp == 1) {
+    } else if (warp == kLoadWarps) {
         if (lane == 0) {
             const uint32_t ty = f16 ? 0u : (1u << 7) | (1u << 10);
             const uint32_t idesc = (1u << 4) | ty | (1u << 15) | (1u << 16) | ((uint32_t)(c.Rq >> 3) << 17) |
@@ -1030,7 +1040,7 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
         }
         __syncwarp();
     } else {
-        const int w = warp - 2;
+        const int w = warp - kLoadWarps - 1;
         bool ok = true;
         if (of_q) {
             // 64-column atom w & 3, rows 32 (w >> 2) .. +31: four chunks of 16 codes a thread; the
@@ -1135,7 +1145,7 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
     }
     __syncthreads();
     cluster_sync();
-    if (warp >= 2) {
+    if (warp > kLoadWarps) {
         // CTA j adds the cluster's parts of its share of the 256 columns, in order
         const int share = 256 / z, row0 = rank * share, pitch = c.Rq + 4;
         const uint32_t mine = smem_u32(smem);
@@ -1145,14 +1155,19 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
         const float sc = of_dy ? p.scales[i] * back : back;
         T* da = static_cast<T*>(p.da);
         T* db = static_cast<T*>(p.db);
-        for (int e = tid - 64; e < share * c.R; e += kGramWork * 32) {
+        for (int e = tid - (kLoadWarps + 1) * 32; e < share * c.R; e += kGramWork * 32) {
             // consecutive threads write consecutive elements: r of dB's rows, columns of dA's
             const int row = row0 + (of_dy ? e / c.R : e % share), r = of_dy ? e % c.R : e / share;
             if (n0 + row >= ncols)
                 continue;
-            float s = 0.f;
-            for (int k = 0; k < z; ++k)
-                s += ld_peer(peer_smem(mine + (uint32_t)(row * pitch + r) * 4u, (uint32_t)k));
+            const uint32_t from = mine + (uint32_t)(row * pitch + r) * 4u;
+            float part[kMaxSplit], s = 0.f;
+#pragma unroll
+            for (int k = 0; k < kMaxSplit; ++k)
+                part[k] = k < z ? ld_peer(peer_smem(from, (uint32_t)k)) : 0.f;
+#pragma unroll
+            for (int k = 0; k < kMaxSplit; ++k)
+                s += part[k];
             const T v = from_float<T>(tokens > 0 ? s * sc : 0.f);
             if (of_dy)
                 db[((size_t)i * p.N + n0 + row) * c.R + r] = v;
@@ -1161,7 +1176,7 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
         }
     }
     cluster_sync();
-    if (warp == 1)
+    if (warp == kLoadWarps)
         tmem_dealloc(tmem, (uint32_t)p.tmem_cols);
 }
 
