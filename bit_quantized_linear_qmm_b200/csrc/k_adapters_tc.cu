@@ -53,12 +53,6 @@ QLIN_DEV float4 ld_peer_v4(uint32_t addr)
                  : "r"(addr));
     return v;
 }
-QLIN_DEV float ld_peer(uint32_t addr)
-{
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
-    return v;
-}
 QLIN_DEV void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -1155,24 +1149,53 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
         const float sc = of_dy ? p.scales[i] * back : back;
         T* da = static_cast<T*>(p.da);
         T* db = static_cast<T*>(p.db);
-        for (int e = tid - (kLoadWarps + 1) * 32; e < share * c.R; e += kGramWork * 32) {
-            // consecutive threads write consecutive elements: r of dB's rows, columns of dA's
-            const int row = row0 + (of_dy ? e / c.R : e % share), r = of_dy ? e % c.R : e / share;
-            if (n0 + row >= ncols)
-                continue;
-            const uint32_t from = mine + (uint32_t)(row * pitch + r) * 4u;
-            float part[kMaxSplit], s = 0.f;
+        const int per = c.R / 4, items = share * per;
+        // item e: four ranks of a column; consecutive threads write consecutive elements, ranks of dB's
+        // rows (8 bytes a thread), columns of dA's (2 bytes, four rows)
+        int row = of_dy ? (tid - (kLoadWarps + 1) * 32) / per : (tid - (kLoadWarps + 1) * 32) % share;
+        int r4 = of_dy ? (tid - (kLoadWarps + 1) * 32) % per : (tid - (kLoadWarps + 1) * 32) / share;
+        const int step_row = of_dy ? kGramWork * 32 / per : 0, step_r4 = of_dy ? kGramWork * 32 % per : kGramWork * 32 / share;
+#pragma unroll 4
+        for (int e = tid - (kLoadWarps + 1) * 32; e < items; e += kGramWork * 32) {
+            const int64_t n = n0 + row0 + row;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (n < ncols && tokens > 0) {
+                const uint32_t from = mine + (uint32_t)((row0 + row) * pitch + 4 * r4) * 4u;
+                if (z == 1) {
+                    s = *reinterpret_cast<const float4*>(smem + (from - mine));
+                } else {
+                    float4 part[kMaxSplit];
 #pragma unroll
-            for (int k = 0; k < kMaxSplit; ++k)
-                part[k] = k < z ? ld_peer(peer_smem(from, (uint32_t)k)) : 0.f;
+                    for (int k = 0; k < kMaxSplit; ++k)
+                        part[k] = k < z ? ld_peer_v4(peer_smem(from, (uint32_t)k)) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int k = 0; k < kMaxSplit; ++k)
-                s += part[k];
-            const T v = from_float<T>(tokens > 0 ? s * sc : 0.f);
-            if (of_dy)
-                db[((size_t)i * p.N + n0 + row) * c.R + r] = v;
-            else
-                da[((size_t)i * c.R + r) * p.K + n0 + row] = v;
+                    for (int k = 0; k < kMaxSplit; ++k) {
+                        s.x += part[k].x;
+                        s.y += part[k].y;
+                        s.z += part[k].z;
+                        s.w += part[k].w;
+                    }
+                }
+                s = make_float4(s.x * sc, s.y * sc, s.z * sc, s.w * sc);
+            }
+            if (n < ncols) {
+                if (of_dy) {
+                    *reinterpret_cast<uint2*>(db + ((size_t)i * p.N + n) * c.R + 4 * r4) =
+                        make_uint2(pack_h16x2(s.x, s.y, f16), pack_h16x2(s.z, s.w, f16));
+                } else {
+                    T* o = da + ((size_t)i * c.R + 4 * r4) * p.K + n;
+                    o[0] = from_float<T>(s.x);
+                    o[p.K] = from_float<T>(s.y);
+                    o[2 * p.K] = from_float<T>(s.z);
+                    o[3 * p.K] = from_float<T>(s.w);
+                }
+            }
+            row += step_row;
+            r4 += step_r4;
+            if (of_dy && r4 >= per) {
+                r4 -= per;
+                ++row;
+            }
         }
     }
     cluster_sync();
