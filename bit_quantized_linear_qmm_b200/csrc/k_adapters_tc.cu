@@ -440,12 +440,14 @@ __global__ void __launch_bounds__(256) adapters_split_kernel(const SplitParams p
 
 // ------------------------------------------------------------------------------------ wide
 
-// out = base + h F: a CTA for each tile and strip of columns, 128 columns at a time.
-//   warps 0..3   the loads: once the halves of h; each block's factor -- forward B_i [128 n][R],
-//                K-major; backward A_i [Rq r][128 k], MN-major -- and base [128 rows][128 columns]
+// out = base + h F, persistent: the (tile, block of 128 columns) units of the batch, tile by tile, in
+// equal contiguous shares, one CTA an SM.  A share is one to a few segments, each of one tile.
+//   warps 0..3   the loads: for a segment the halves of h; each block's factor -- forward B_i
+//                [128 n][R], K-major; backward A_i [Rq r][128 k], MN-major -- and base [128][128]
 //   warp 4       two accumulators of 128 columns; hi and lo halves on the same factor block
 //   warps 5..12  32 rows by 64 columns each: the sum, scaled, onto base in shared memory, then out in
-//                whole 128-byte pieces of a row (base's own place serves as the staging buffer)
+//                whole 128-byte pieces of a row (base's own place serves as the staging buffer);
+//                rows of tokens without an adapter are copied here, or left when out is base
 constexpr int kWideEpi = 8;
 constexpr int kWideThreads = (kLoadWarps + 1 + kWideEpi) * 32;
 constexpr int kWideMaxStages = 4;
@@ -459,7 +461,7 @@ struct WideParams {
     const void* base_p;   // null: zeros
     void* out;
     int64_t N;
-    int strip;            // columns of a CTA, a multiple of 128
+    int blocks;           // of a row
     int stages, f_bytes;
 };
 
@@ -469,7 +471,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapters_wide_kernel(const __
     constexpr int f16 = Is16<T>::f16;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t full[kWideMaxStages], empty[kWideMaxStages], acc_full[2], acc_empty[2], h_full;
+    __shared__ uint64_t full[kWideMaxStages], empty[kWideMaxStages], acc_full[2], acc_empty[2], h_full, h_empty;
     __shared__ uint32_t tmem_s;
     __shared__ int abort_flag;
     const Common& c = p.c;
@@ -484,28 +486,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapters_wide_kernel(const __
             mbar_init(&acc_empty[b], kWideEpi);
         }
         mbar_init(&h_full, 1);
+        mbar_init(&h_empty, 1);
         abort_flag = 0;
         fence_mbar_init();
-    }
-    pdl_wait_prior_grids();
-    const int t = blockIdx.y;
-    if (t >= c.plan.head[3])
-        return;
-    const AdapterTile d = c.plan.tiles_l[t];
-    const int64_t n_begin = (int64_t)blockIdx.x * p.strip;
-    const int64_t n_end = n_begin + p.strip < p.N ? n_begin + p.strip : p.N;
-    T* out = static_cast<T*>(p.out);
-    if (d.adapter >= c.L) {
-        if (p.base_p == p.out)
-            return;
-        const T* base = static_cast<const T*>(p.base_p);
-        const int vecs = (int)((n_end - n_begin) / 8);
-        for (int i = tid; i < d.count * vecs; i += kWideThreads) {
-            const size_t at = (size_t)c.plan.perm[d.start + i / vecs] * p.N + n_begin + 8 * (i % vecs);
-            *reinterpret_cast<uint4*>(out + at) =
-                base ? *reinterpret_cast<const uint4*>(base + at) : make_uint4(0u, 0u, 0u, 0u);
-        }
-        return;
     }
     if (warp == kLoadWarps)
         tmem_alloc(&tmem_s, 2 * kWideCols);
@@ -513,83 +496,120 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapters_wide_kernel(const __
     __syncthreads();
     tc_fence_after();
     pdl_launch_dependents();  // after the allocation, as in the narrow kernel
+    pdl_wait_prior_grids();
     const uint32_t tmem = tmem_s;
-    const int blocks = (int)((n_end - n_begin + kWideCols - 1) / kWideCols);
     const int atoms = (c.Rq + 63) / 64, h_half = atoms * 2 * (int)kAtom;
     constexpr int base_bytes = 4 * (int)kAtom;
     const int stage_bytes = base_bytes + p.f_bytes;
     uint8_t* Hs = smem;  // hi, then lo: [atoms][128 rows][128 bytes]
     auto B = [&](int s) { return smem + 2 * h_half + s * stage_bytes; };
     auto F = [&](int s) { return smem + 2 * h_half + s * stage_bytes + base_bytes; };
+    // this CTA's units; tiles of tokens without an adapter come last and count where they are copied
+    const int64_t units = (int64_t)c.plan.head[p.base_p == p.out ? 5 : 3] * p.blocks;
+    const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+    // blocks b0 .. b1 - 1 of the tile that unit u belongs to
+    auto segment = [&](int64_t u, int& t, int& b0, int& b1) {
+        t = (int)(u / p.blocks);
+        b0 = (int)(u - (int64_t)t * p.blocks);
+        b1 = (int)(u1 - u < p.blocks - b0 ? b0 + (u1 - u) : p.blocks);
+    };
 
     if (warp < kLoadWarps) {
-        const int piece = 16 * (warp & 1) + lane;  // lanes 0..15: four rows each of a gathered 64-column half
-        const bool box = d.first >= 0;
-        const int4 tok = box || lane >= 16 ? make_int4(0, 0, 0, 0) : row_tokens(c.plan, d.start, d.count, piece);
-        if (tid == 0) {
-            mbar_arrive_expect_tx(&h_full, 2u * (unsigned)h_half);
-            for (int half = 0; half < 2; ++half)
-                for (int a = 0; a < atoms; ++a)
-                    tma_load_2d(Hs + half * h_half + a * 2 * kAtom, &p.tm_h, a * 64, (int)(half * c.slots) + t * kTileL, &h_full);
-        }
-        int it = 0;
-        for (; it < blocks && (warp == 0 || (!box && p.base_p)); ++it) {
-            const int slot = it % p.stages;
-            const bool ok = it < p.stages || mbar_wait_bounded(&empty[slot], ((it / p.stages) & 1) ^ 1, c.status);
-            if (__any_sync(0xffffffffu, !ok || aborted(&abort_flag))) {
-                abort_flag = 1;
-                break;
-            }
-            const int n = (int)n_begin + it * kWideCols;
-            if (tid == 0) {
-                mbar_arrive_expect_tx(&full[slot], (unsigned)(p.f_bytes + (p.base_p ? base_bytes : 0)));
-                if constexpr (FWD) {
-                    for (int a = 0; a < atoms; ++a)
-                        tma_load_3d(F(slot) + a * 2 * kAtom, &p.tm_f, a * 64, n, d.adapter, &full[slot]);
-                } else {
-                    for (int a = 0; a < 2; ++a)
-                        tma_load_3d(F(slot) + a * c.Rq * 128, &p.tm_f, n + a * 64, 0, d.adapter, &full[slot]);
+        const int piece = 16 * (warp & 1) + (lane & 15);  // lanes 0..15: four rows each of a gathered 64-column half
+        int it = 0, seg = 0;
+        bool ok = true;
+        for (int64_t u = u0; u < u1 && ok;) {
+            int t, b0, b1;
+            segment(u, t, b0, b1);
+            u += b1 - b0;
+            const AdapterTile d = c.plan.tiles_l[t];
+            if (d.adapter >= c.L)
+                break;  // and so are all that follow
+            const bool box = d.first >= 0;
+            const int4 tok = box ? make_int4(0, 0, 0, 0) : row_tokens(c.plan, d.start, d.count, piece);
+            if (warp == 0) {  // h of the segment, once the MMAs of the last one are done
+                if (seg > 0 && !mbar_wait_bounded(&h_empty, (seg & 1) ^ 1, c.status))
+                    ok = false;
+                if (ok && lane == 0) {
+                    mbar_arrive_expect_tx(&h_full, 2u * (unsigned)h_half);
+                    for (int half = 0; half < 2; ++half)
+                        for (int a = 0; a < atoms; ++a)
+                            tma_load_2d(Hs + half * h_half + a * 2 * kAtom, &p.tm_h, a * 64,
+                                        (int)(half * c.slots) + t * kTileL, &h_full);
                 }
-                if (box && p.base_p)
-                    for (int a = 0; a < 2; ++a)
-                        load_box(smem_u32(B(slot)) + a * 2 * kAtom, p.base, n + a * 64, d.first, 2, &full[slot]);
+                ++seg;
             }
-            __syncwarp();
-            if (!box && p.base_p && lane < 16) {
-                const int a = warp >> 1;
-                tma_gather4(smem_u32(B(slot)) + a * 2 * kAtom + piece * 512, &p.base.row, n + a * 64, tok, &full[slot]);
+            for (int b = b0; b < b1 && ok; ++b, ++it) {
+                const int slot = it % p.stages;
+                ok = it < p.stages || mbar_wait_bounded(&empty[slot], ((it / p.stages) & 1) ^ 1, c.status);
+                ok = __all_sync(0xffffffffu, ok && !aborted(&abort_flag));
+                if (!ok)
+                    break;
+                const int n = b * kWideCols;
+                if (tid == 0) {
+                    mbar_arrive_expect_tx(&full[slot], (unsigned)(p.f_bytes + (p.base_p ? base_bytes : 0)));
+                    if (box && p.base_p)
+                        for (int a = 0; a < 2; ++a)
+                            load_box(smem_u32(B(slot)) + a * 2 * kAtom, p.base, n + a * 64, d.first, 2, &full[slot]);
+                    if constexpr (FWD) {
+                        for (int a = 0; a < atoms; ++a)
+                            tma_load_3d(F(slot) + a * 2 * kAtom, &p.tm_f, a * 64, n, d.adapter, &full[slot]);
+                    } else {
+                        for (int a = 0; a < 2; ++a)
+                            tma_load_3d(F(slot) + a * c.Rq * 128, &p.tm_f, n + a * 64, 0, d.adapter, &full[slot]);
+                    }
+                }
+                __syncwarp();
+                if (!box && p.base_p && lane < 16) {
+                    const int a = warp >> 1;
+                    tma_gather4(smem_u32(B(slot)) + a * 2 * kAtom + piece * 512, &p.base.row, n + a * 64, tok, &full[slot]);
+                }
             }
         }
-        mbar_wait_bounded(&h_full, 0, c.status);
-        for (int j = it - p.stages < 0 ? 0 : it - p.stages; j < it; ++j)
-            mbar_wait_bounded(&full[j % p.stages], (j / p.stages) & 1, c.status);
+        if (!ok)
+            abort_flag = 1;
+        if (warp == 0) {  // no copy may land after the exit
+            if (seg > 0)
+                mbar_wait_bounded(&h_full, (seg - 1) & 1, c.status);
+            for (int j = it - p.stages < 0 ? 0 : it - p.stages; j < it; ++j)
+                mbar_wait_bounded(&full[j % p.stages], (j / p.stages) & 1, c.status);
+        }
     } else if (warp == kLoadWarps) {
         if (lane == 0) {
             const uint32_t ty = f16 ? 0u : (1u << 7) | (1u << 10);
             const uint32_t idesc = (1u << 4) | ty | (FWD ? 0u : 1u << 16) | ((uint32_t)(kWideCols >> 3) << 17) |
                                    ((uint32_t)(128 >> 4) << 24);
-            bool ok = mbar_wait_bounded(&h_full, 0, c.status);
-            int last = -1;
-            for (int it = 0; it < blocks && ok; ++it) {
-                const int slot = it % p.stages, buf = it & 1;
-                ok = mbar_wait_bounded(&acc_empty[buf], ((it >> 1) & 1) ^ 1, c.status) &&
-                     mbar_wait_bounded(&full[slot], (it / p.stages) & 1, c.status);
-                if (!ok)
+            bool ok = true;
+            int it = 0, seg = 0, last = -1;
+            for (int64_t u = u0; u < u1 && ok; ++seg) {
+                int t, b0, b1;
+                segment(u, t, b0, b1);
+                u += b1 - b0;
+                if (c.plan.tiles_l[t].adapter >= c.L)
                     break;
-                tc_fence_after();
-                const uint32_t h = smem_u32(Hs), f = smem_u32(F(slot));
-                for (int kk = 0; kk < c.Rq / 16; ++kk) {
-                    const uint64_t fd = FWD ? umma_desc_sw128(f + (kk >> 2) * 2 * kAtom + (kk & 3) * 32)
-                                            : umma_desc_sw128_mn(f + kk * 2048, (uint32_t)(c.Rq * 128));
+                ok = mbar_wait_bounded(&h_full, seg & 1, c.status);
+                for (int b = b0; b < b1 && ok; ++b, ++it) {
+                    const int slot = it % p.stages, buf = it & 1;
+                    ok = mbar_wait_bounded(&acc_empty[buf], ((it >> 1) & 1) ^ 1, c.status) &&
+                         mbar_wait_bounded(&full[slot], (it / p.stages) & 1, c.status);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    const uint32_t h = smem_u32(Hs), f = smem_u32(F(slot));
+                    for (int kk = 0; kk < c.Rq / 16; ++kk) {
+                        const uint64_t fd = FWD ? umma_desc_sw128(f + (kk >> 2) * 2 * kAtom + (kk & 3) * 32)
+                                                : umma_desc_sw128_mn(f + kk * 2048, (uint32_t)(c.Rq * 128));
 #pragma unroll
-                    for (int half = 0; half < 2; ++half)
-                        tc_mma<false>(tmem + (uint32_t)(buf * kWideCols),
-                                      umma_desc_sw128(h + half * h_half + (kk >> 2) * 2 * kAtom + (kk & 3) * 32), fd,
-                                      idesc, (kk | half) != 0 ? 1u : 0u);
+                        for (int half = 0; half < 2; ++half)
+                            tc_mma<false>(tmem + (uint32_t)(buf * kWideCols),
+                                          umma_desc_sw128(h + half * h_half + (kk >> 2) * 2 * kAtom + (kk & 3) * 32), fd,
+                                          idesc, (kk | half) != 0 ? 1u : 0u);
+                    }
+                    tc_commit(&empty[slot]);
+                    tc_commit(&acc_full[buf]);
+                    last = it;
                 }
-                tc_commit(&empty[slot]);
-                tc_commit(&acc_full[buf]);
-                last = it;
+                tc_commit(&h_empty);
             }
             if (!ok)
                 abort_flag = 1;
@@ -598,57 +618,91 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapters_wide_kernel(const __
         }
         __syncwarp();
     } else {
-        const int q = warp & 3, half = (warp - kLoadWarps - 1) >> 2, row = 32 * q + lane;
-        const int my_tok = row < d.count ? c.plan.perm[d.start + row] : -1;
-        float rs = FWD ? p.scales[d.adapter] : 1.f;
-        if constexpr (f16)
-            rs *= __ldcg(c.row_back + (size_t)t * kTileL + row);
-        for (int it = 0; it < blocks; ++it) {
-            const int slot = it % p.stages, buf = it & 1;
-            if (!mbar_wait_bounded(&full[slot], (it / p.stages) & 1, c.status) ||
-                !mbar_wait_bounded(&acc_full[buf], (it >> 1) & 1, c.status) || aborted(&abort_flag)) {
-                abort_flag = 1;
-                break;
+        const int w = warp - kLoadWarps - 1, q = warp & 3, half = w >> 2, row = 32 * q + lane;
+        T* out = static_cast<T*>(p.out);
+        const T* base = static_cast<const T*>(p.base_p);
+        int it = 0;
+        bool ok = true;
+        for (int64_t u = u0; u < u1 && ok;) {
+            int t, b0, b1;
+            segment(u, t, b0, b1);
+            u += b1 - b0;
+            const AdapterTile d = c.plan.tiles_l[t];
+            if (d.adapter >= c.L) {
+                // a warp copies 16 rows of a block, two rows of 256 bytes an instruction, eight in flight
+                const int r0 = 16 * w + (lane & 15);
+                const int mine = r0 < d.count ? c.plan.perm[d.start + r0] : -1;
+                for (int b = b0; b < b1; ++b) {
+                    const int64_t n = (int64_t)b * kWideCols + 8 * (lane & 15);
+                    uint4 v[8];
+                    int tok[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        tok[e] = __shfl_sync(0xffffffffu, mine, 2 * e + (lane >> 4));
+                        v[e] = base && tok[e] >= 0 && n < p.N
+                                   ? *reinterpret_cast<const uint4*>(base + (size_t)tok[e] * p.N + n)
+                                   : make_uint4(0u, 0u, 0u, 0u);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (tok[e] >= 0 && n < p.N)
+                            *reinterpret_cast<uint4*>(out + (size_t)tok[e] * p.N + n) = v[e];
+                }
+                continue;
             }
-            tc_fence_after();
-            const uint32_t acc = tmem + (uint32_t)(buf * kWideCols + half * 64) + ((uint32_t)(32 * q) << 16);
-            uint8_t* at = B(slot) + half * 2 * kAtom;
-            uint32_t r[4][16];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                tmem_ld16_nowait(acc + 16u * e, r[e]);
-            tmem_wait_ld();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&acc_empty[buf]);
-#pragma unroll
-            for (int un = 0; un < 8; ++un) {
-                uint4* b = reinterpret_cast<uint4*>(at + swz128(row, un));
-                const uint4 bv = p.base_p ? *b : make_uint4(0u, 0u, 0u, 0u);
-                const uint32_t bw[4] = {bv.x, bv.y, bv.z, bv.w};
-                uint32_t o[4];
+            const int my_tok = row < d.count ? c.plan.perm[d.start + row] : -1;
+            float rs = FWD ? p.scales[d.adapter] : 1.f;
+            if constexpr (f16)
+                rs *= __ldcg(c.row_back + (size_t)t * kTileL + row);
+            for (int b = b0; b < b1; ++b, ++it) {
+                const int slot = it % p.stages, buf = it & 1;
+                if (!mbar_wait_bounded(&full[slot], (it / p.stages) & 1, c.status) ||
+                    !mbar_wait_bounded(&acc_full[buf], (it >> 1) & 1, c.status) || aborted(&abort_flag)) {
+                    abort_flag = 1;
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t acc = tmem + (uint32_t)(buf * kWideCols + half * 64) + ((uint32_t)(32 * q) << 16);
+                uint8_t* at = B(slot) + half * 2 * kAtom;
+                uint32_t r[4][16];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    o[e] = pack_h16x2(
-                        fmaf(__uint_as_float(r[un >> 1][(un & 1) * 8 + 2 * e]), rs, h16_to_float(bw[e], f16)),
-                        fmaf(__uint_as_float(r[un >> 1][(un & 1) * 8 + 2 * e + 1]), rs, h16_to_float(bw[e] >> 16, f16)), f16);
-                *b = make_uint4(o[0], o[1], o[2], o[3]);
-            }
-            __syncwarp();
-            const int64_t n = n_begin + it * kWideCols + half * 64 + 8 * (lane & 7);
+                    tmem_ld16_nowait(acc + 16u * e, r[e]);
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&acc_empty[buf]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int rr = 4 * e + (lane >> 3);
-                const int tok = __shfl_sync(0xffffffffu, my_tok, rr);
-                const uint4 v = *reinterpret_cast<const uint4*>(at + swz128(32 * q + rr, lane & 7));
-                if (tok >= 0 && n < p.N)
-                    *reinterpret_cast<uint4*>(out + (size_t)tok * p.N + n) = v;
+                for (int un = 0; un < 8; ++un) {
+                    uint4* bp = reinterpret_cast<uint4*>(at + swz128(row, un));
+                    const uint4 bv = p.base_p ? *bp : make_uint4(0u, 0u, 0u, 0u);
+                    const uint32_t bw[4] = {bv.x, bv.y, bv.z, bv.w};
+                    uint32_t o[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o[e] = pack_h16x2(
+                            fmaf(__uint_as_float(r[un >> 1][(un & 1) * 8 + 2 * e]), rs, h16_to_float(bw[e], f16)),
+                            fmaf(__uint_as_float(r[un >> 1][(un & 1) * 8 + 2 * e + 1]), rs, h16_to_float(bw[e] >> 16, f16)),
+                            f16);
+                    *bp = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+                __syncwarp();
+                const int64_t n = (int64_t)b * kWideCols + half * 64 + 8 * (lane & 7);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int rr = 4 * e + (lane >> 3);
+                    const int tok = __shfl_sync(0xffffffffu, my_tok, rr);
+                    const uint4 v = *reinterpret_cast<const uint4*>(at + swz128(32 * q + rr, lane & 7));
+                    if (tok >= 0 && n < p.N)
+                        *reinterpret_cast<uint4*>(out + (size_t)tok * p.N + n) = v;
+                }
+                fence_proxy_async_smem();  // the next copy into this place comes after these accesses
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&empty[slot]);
             }
-            fence_proxy_async_smem();  // the next copy into this place comes after these accesses
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&empty[slot]);
         }
     }
     tc_fence_before();
@@ -1043,23 +1097,31 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
             const int unit = (atom & 1) * 4 + (lane & 3), bunit = 2 * (lane & 3), swap = (lane >> 2) & 1;
             const int64_t k = n0 + atom * 64;
             const float* sc = k < p.K ? p.q_scale + (k >> p.g_shift) * c.M : nullptr;
+            // a step's tokens are read two steps ahead, their scales one
             float next[4];
-            auto load_scales = [&](int it) {
+            int tok[4];
+            auto load_tokens = [&](int it) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int row = row0 + 8 * e;
-                    next[e] = it < n_st && sc && row < rows_of(it)
-                                  ? __ldg(sc + c.plan.perm[seg0 + (rank + it * z) * 64 + row])
-                                  : 0.f;
+                    tok[e] = it < n_st && sc && row < rows_of(it) ? c.plan.perm[seg0 + (rank + it * z) * 64 + row] : -1;
                 }
             };
-            load_scales(0);
+            auto load_scales = [&]() {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    next[e] = tok[e] >= 0 ? __ldg(sc + tok[e]) : 0.f;
+            };
+            load_tokens(0);
+            load_scales();
+            load_tokens(1);
             for (int it = 0; it < n_st; ++it) {
                 float s[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     s[e] = next[e];
-                load_scales(it + 1);
+                load_scales();
+                load_tokens(it + 2);
                 const int slot = it % stages, b = it & 1;
                 if (!mbar_wait_bounded(&full[slot], (it / stages) & 1, c.status) ||
                     (it >= 2 && !mbar_wait_bounded(&taken[b], ((it >> 1) & 1) ^ 1, c.status)) || aborted(&abort_flag)) {
@@ -1357,11 +1419,9 @@ cudaError_t launch_wide(const Common& c, const void* f, const float* scales, con
     const int stage = 4 * (int)kAtom + p.f_bytes, room = 224 * 1024 - h;
     p.stages = room / stage < kWideMaxStages ? room / stage : kWideMaxStages;
     const int64_t tiles = max_tiles(c.M, c.L, kTileL);
-    // strips of 4096 columns, shorter while that leaves fewer than two CTAs an SM
-    p.strip = 4096;
-    while (p.strip > kWideCols && tiles * ((N + p.strip - 1) / p.strip) < 2 * dev.sm_count)
-        p.strip /= 2;
-    const dim3 grid((unsigned)((N + p.strip - 1) / p.strip), (unsigned)tiles);
+    p.blocks = (int)((N + kWideCols - 1) / kWideCols);
+    const int64_t units = tiles * p.blocks;
+    const dim3 grid((unsigned)(units < dev.sm_count ? units : dev.sm_count));
     return launch(adapters_wide_kernel<T, FWD>, grid, kWideThreads, h + p.stages * stage + 1024, 0, p, st);
 }
 
