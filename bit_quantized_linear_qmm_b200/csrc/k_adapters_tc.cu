@@ -446,8 +446,9 @@ __global__ void __launch_bounds__(256) adapters_split_kernel(const SplitParams p
 //                [128 n][R], K-major; backward A_i [Rq r][128 k], MN-major -- and base [128][128]
 //   warp 4       two accumulators of 128 columns; hi and lo halves on the same factor block
 //   warps 5..12  32 rows by 64 columns each: the sum, scaled, onto base in shared memory, then out in
-//                whole 128-byte pieces of a row (base's own place serves as the staging buffer);
-//                rows of tokens without an adapter are copied here, or left when out is base
+//                whole 128-byte pieces of a row (base's own place serves as the staging buffer)
+// Tiles of tokens without an adapter pass through without a product (their rows are copied as they
+// are), or are left out when out is base itself.
 constexpr int kWideEpi = 8;
 constexpr int kWideThreads = (kLoadWarps + 1 + kWideEpi) * 32;
 constexpr int kWideMaxStages = 4;
@@ -523,11 +524,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapters_wide_kernel(const __
             segment(u, t, b0, b1);
             u += b1 - b0;
             const AdapterTile d = c.plan.tiles_l[t];
-            if (d.adapter >= c.L)
-                break;  // and so are all that follow
+            const bool none = d.adapter >= c.L;
             const bool box = d.first >= 0;
             const int4 tok = box ? make_int4(0, 0, 0, 0) : row_tokens(c.plan, d.start, d.count, piece);
-            if (warp == 0) {  // h of the segment, once the MMAs of the last one are done
+            if (warp == 0 && !none) {  // h of the segment, once the MMAs of the last one are done
                 if (seg > 0 && !mbar_wait_bounded(&h_empty, (seg & 1) ^ 1, c.status))
                     ok = false;
                 if (ok && lane == 0) {
@@ -547,11 +547,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapters_wide_kernel(const __
                     break;
                 const int n = b * kWideCols;
                 if (tid == 0) {
-                    mbar_arrive_expect_tx(&full[slot], (unsigned)(p.f_bytes + (p.base_p ? base_bytes : 0)));
+                    mbar_arrive_expect_tx(&full[slot], (unsigned)((none ? 0 : p.f_bytes) + (p.base_p ? base_bytes : 0)));
                     if (box && p.base_p)
                         for (int a = 0; a < 2; ++a)
                             load_box(smem_u32(B(slot)) + a * 2 * kAtom, p.base, n + a * 64, d.first, 2, &full[slot]);
-                    if constexpr (FWD) {
+                    if (none) {
+                    } else if constexpr (FWD) {
                         for (int a = 0; a < atoms; ++a)
                             tma_load_3d(F(slot) + a * 2 * kAtom, &p.tm_f, a * 64, n, d.adapter, &full[slot]);
                     } else {
@@ -581,13 +582,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapters_wide_kernel(const __
                                    ((uint32_t)(128 >> 4) << 24);
             bool ok = true;
             int it = 0, seg = 0, last = -1;
-            for (int64_t u = u0; u < u1 && ok; ++seg) {
+            for (int64_t u = u0; u < u1 && ok;) {
                 int t, b0, b1;
                 segment(u, t, b0, b1);
                 u += b1 - b0;
-                if (c.plan.tiles_l[t].adapter >= c.L)
-                    break;
-                ok = mbar_wait_bounded(&h_full, seg & 1, c.status);
+                const bool none = c.plan.tiles_l[t].adapter >= c.L;
+                ok = none || mbar_wait_bounded(&h_full, seg & 1, c.status);
                 for (int b = b0; b < b1 && ok; ++b, ++it) {
                     const int slot = it % p.stages, buf = it & 1;
                     ok = mbar_wait_bounded(&acc_empty[buf], ((it >> 1) & 1) ^ 1, c.status) &&
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapters_wide_kernel(const __
                         break;
                     tc_fence_after();
                     const uint32_t h = smem_u32(Hs), f = smem_u32(F(slot));
-                    for (int kk = 0; kk < c.Rq / 16; ++kk) {
+                    for (int kk = 0; kk < (none ? 0 : c.Rq / 16); ++kk) {
                         const uint64_t fd = FWD ? umma_desc_sw128(f + (kk >> 2) * 2 * kAtom + (kk & 3) * 32)
                                                 : umma_desc_sw128_mn(f + kk * 2048, (uint32_t)(c.Rq * 128));
 #pragma unroll
@@ -609,7 +609,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapters_wide_kernel(const __
                     tc_commit(&acc_full[buf]);
                     last = it;
                 }
-                tc_commit(&h_empty);
+                if (!none) {
+                    tc_commit(&h_empty);
+                    ++seg;
+                }
             }
             if (!ok)
                 abort_flag = 1;
@@ -620,7 +623,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapters_wide_kernel(const __
     } else {
         const int w = warp - kLoadWarps - 1, q = warp & 3, half = w >> 2, row = 32 * q + lane;
         T* out = static_cast<T*>(p.out);
-        const T* base = static_cast<const T*>(p.base_p);
         int it = 0;
         bool ok = true;
         for (int64_t u = u0; u < u1 && ok;) {
@@ -628,32 +630,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapters_wide_kernel(const __
             segment(u, t, b0, b1);
             u += b1 - b0;
             const AdapterTile d = c.plan.tiles_l[t];
-            if (d.adapter >= c.L) {
-                // a warp copies 16 rows of a block, two rows of 256 bytes an instruction, eight in flight
-                const int r0 = 16 * w + (lane & 15);
-                const int mine = r0 < d.count ? c.plan.perm[d.start + r0] : -1;
-                for (int b = b0; b < b1; ++b) {
-                    const int64_t n = (int64_t)b * kWideCols + 8 * (lane & 15);
-                    uint4 v[8];
-                    int tok[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        tok[e] = __shfl_sync(0xffffffffu, mine, 2 * e + (lane >> 4));
-                        v[e] = base && tok[e] >= 0 && n < p.N
-                                   ? *reinterpret_cast<const uint4*>(base + (size_t)tok[e] * p.N + n)
-                                   : make_uint4(0u, 0u, 0u, 0u);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (tok[e] >= 0 && n < p.N)
-                            *reinterpret_cast<uint4*>(out + (size_t)tok[e] * p.N + n) = v[e];
-                }
-                continue;
-            }
+            const bool none = d.adapter >= c.L;
             const int my_tok = row < d.count ? c.plan.perm[d.start + row] : -1;
-            float rs = FWD ? p.scales[d.adapter] : 1.f;
+            float rs = FWD && !none ? p.scales[d.adapter] : 1.f;
             if constexpr (f16)
-                rs *= __ldcg(c.row_back + (size_t)t * kTileL + row);
+                rs *= none ? 1.f : __ldcg(c.row_back + (size_t)t * kTileL + row);
             for (int b = b0; b < b1; ++b, ++it) {
                 const int slot = it % p.stages, buf = it & 1;
                 if (!mbar_wait_bounded(&full[slot], (it / p.stages) & 1, c.status) ||
@@ -678,6 +659,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapters_wide_kernel(const __
                 for (int un = 0; un < 8; ++un) {
                     uint4* bp = reinterpret_cast<uint4*>(at + swz128(row, un));
                     const uint4 bv = p.base_p ? *bp : make_uint4(0u, 0u, 0u, 0u);
+                    if (none) {
+                        if (!p.base_p)
+                            *bp = bv;
+                        continue;
+                    }
                     const uint32_t bw[4] = {bv.x, bv.y, bv.z, bv.w};
                     uint32_t o[4];
 #pragma unroll
