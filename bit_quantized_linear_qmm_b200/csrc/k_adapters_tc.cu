@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(kNarrowThreads) adapters_narrow_kernel(const _
     __shared__ uint32_t tmem_s;
     __shared__ int abort_flag;
     __shared__ float warp_max[2][4];
+    __shared__ int toks[kTileL];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int z = gridDim.x, rank = blockIdx.x;  // the cluster spans the grid's x
     const int stage_bytes = 2 * (int)kAtom + p.f_bytes;
@@ -281,8 +282,40 @@ __global__ void __launch_bounds__(kNarrowThreads) adapters_narrow_kernel(const _
         }
         __syncwarp();
     } else {
-        // this CTA's sums, [128][Rq], into the ring's memory (every MMA, so every copy, is done)
         const int q = warp & 3;
+        // during the products: the tokens of this CTA's rows, and (backward) its rows of u
+        for (int i = tid - (kLoadWarps + 1) * 32; i < rows; i += 128)
+            toks[i] = row0 + i < d.count ? c.plan.perm[d.start + row0 + i] : -1;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if constexpr (!FWD) {
+            const int per = c.Rq / 4;
+            const size_t lo_at = (size_t)c.slots * c.Rq;
+            float umax = 0.f;
+            for (int i = tid - (kLoadWarps + 1) * 32; i < rows * per; i += 128) {
+                const int row = i / per, col = 4 * (i % per);
+                const size_t at = ((size_t)t * kTileL + row0 + row) * c.Rq + col;
+                float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (toks[row] >= 0 && col < c.R)
+                    u = __ldg(reinterpret_cast<const float4*>(p.u_in + (size_t)toks[row] * c.R + col));
+                if constexpr (f16) {
+                    umax = fmaxf(umax, fmaxf(fmaxf(finite_abs(u.x), finite_abs(u.y)), fmaxf(finite_abs(u.z), finite_abs(u.w))));
+                } else {
+                    uint2 hi, lo;
+                    split2<T>(u.x, u.y, hi.x, lo.x);
+                    split2<T>(u.z, u.w, hi.y, lo.y);
+                    *reinterpret_cast<uint2*>(c.u_halves + at) = hi;
+                    *reinterpret_cast<uint2*>(c.u_halves + lo_at + at) = lo;
+                }
+            }
+            if constexpr (f16) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    umax = fmaxf(umax, __shfl_xor_sync(0xffffffffu, umax, o));
+                if (lane == 0)
+                    warp_max[1][warp - kLoadWarps - 1] = umax;
+            }
+        }
+        // this CTA's sums, [128][Rq], into the ring's memory (every MMA, so every copy, is done)
         const bool sums = n_st > 0 && mbar_wait_bounded(&acc_full, 0, c.status) && !aborted(&abort_flag);
         tc_fence_after();
         float* red = reinterpret_cast<float*>(smem) + (size_t)(32 * q + lane) * pitch;
@@ -310,21 +343,18 @@ __global__ void __launch_bounds__(kNarrowThreads) adapters_narrow_kernel(const _
         const int lanes = c.Rq <= 16 ? 4 : c.Rq <= 32 ? 8 : c.Rq <= 64 ? 16 : 32, at_once = 4 * (32 / lanes);
         const int col = 4 * (lane & (lanes - 1));
         const size_t lo_at = (size_t)c.slots * c.Rq;
-        float vmax = 0.f, umax = 0.f;
+        float vmax = 0.f;
         for (int r0 = 0; r0 < rows; r0 += at_once) {
             const int row = row0 + r0 + (warp - kLoadWarps - 1) * (32 / lanes) + lane / lanes;
             const bool mine_ok = row < row0 + rows, in = mine_ok && row < d.count && col < c.R;
             const size_t at = ((size_t)t * kTileL + row) * c.Rq + col;
-            const size_t tok = in ? (size_t)c.plan.perm[d.start + row] : 0;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f), u = s;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
             if (in) {
                 const uint32_t from = mine + (uint32_t)(row * pitch + col) * 4u;
                 float4 v[kMaxSplit];
 #pragma unroll
                 for (int j = 0; j < kMaxSplit; ++j)
                     v[j] = j < z ? ld_peer_v4(peer_smem(from, (uint32_t)j)) : make_float4(0.f, 0.f, 0.f, 0.f);
-                if (!FWD)
-                    u = __ldg(reinterpret_cast<const float4*>(p.u_in + tok * c.R + col));
 #pragma unroll
                 for (int j = 0; j < kMaxSplit; ++j) {
                     s.x += v[j].x;
@@ -334,13 +364,12 @@ __global__ void __launch_bounds__(kNarrowThreads) adapters_narrow_kernel(const _
                 }
                 s = make_float4(sc * s.x, sc * s.y, sc * s.z, sc * s.w);
                 if (FWD && p.u_out)
-                    *reinterpret_cast<float4*>(p.u_out + tok * c.R + col) = s;
+                    *reinterpret_cast<float4*>(p.u_out + (size_t)toks[row - row0] * c.R + col) = s;
             }
             float to = 1.f, back = 1.f;
             if constexpr (f16) {
                 float top = fmaxf(fmaxf(finite_abs(s.x), finite_abs(s.y)), fmaxf(finite_abs(s.z), finite_abs(s.w)));
                 vmax = fmaxf(vmax, top);
-                umax = fmaxf(umax, fmaxf(fmaxf(finite_abs(u.x), finite_abs(u.y)), fmaxf(finite_abs(u.z), finite_abs(u.w))));
                 for (int o = lanes >> 1; o > 0; o >>= 1)
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                 half_scale<T>(top, to, back);
@@ -353,26 +382,16 @@ __global__ void __launch_bounds__(kNarrowThreads) adapters_narrow_kernel(const _
                 split2<T>(s.z * to, s.w * to, hi.y, lo.y);
                 *reinterpret_cast<uint2*>(c.row_halves + at) = hi;
                 *reinterpret_cast<uint2*>(c.row_halves + lo_at + at) = lo;
-                if constexpr (!FWD && f16) {
+                if constexpr (!FWD && f16)
                     *reinterpret_cast<float4*>(c.v + at) = s;
-                } else if constexpr (!FWD) {
-                    split2<T>(u.x, u.y, hi.x, lo.x);
-                    split2<T>(u.z, u.w, hi.y, lo.y);
-                    *reinterpret_cast<uint2*>(c.u_halves + at) = hi;
-                    *reinterpret_cast<uint2*>(c.u_halves + lo_at + at) = lo;
-                }
             }
         }
         if constexpr (!FWD && f16) {
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
+            for (int o = 16; o > 0; o >>= 1)
                 vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
-                umax = fmaxf(umax, __shfl_xor_sync(0xffffffffu, umax, o));
-            }
-            if (lane == 0) {
+            if (lane == 0)
                 warp_max[0][warp - kLoadWarps - 1] = vmax;
-                warp_max[1][warp - kLoadWarps - 1] = umax;
-            }
             asm volatile("bar.sync 1, 128;" ::: "memory");
             const int which = tid - (kLoadWarps + 1) * 32;
             if (which < 2) {
