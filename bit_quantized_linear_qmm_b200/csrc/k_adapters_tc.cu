@@ -951,10 +951,10 @@ __global__ void __launch_bounds__(kDecodeWarps * 32) adapters_decode_kernel(cons
 // for both operands; nothing is transposed.
 //   warps 0..3   the loads: S in 64-column boxes or gathers (codes: 128-byte ones), H in 64-rank boxes
 //   warp 4       tensor memory, the MMAs (two of M = 128 for hi and for lo, N = Rq, K = 16)
-//   warps 5..12  codes: s q in fp32, rounded once to the operand type, into a ring of two buffers;
+//   warps 5..20  codes: s q in fp32, rounded once to the operand type, into a ring of two buffers;
 //                rows past the adapter's last token: zeros (only there, so what another adapter's
 //                row holds enters no sum); then the epilogue
-constexpr int kGramWork = 8;
+constexpr int kGramWork = 16;  // 8 took 1950 cycles to decode a step, twice what its loads take
 constexpr int kGramThreads = (kLoadWarps + 1 + kGramWork) * 32;
 constexpr int kGramMaxStages = 6;
 
@@ -1096,34 +1096,34 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
         const int w = warp - kLoadWarps - 1;
         bool ok = true;
         if (of_q) {
-            // 64-column atom w & 3, rows 32 (w >> 2) .. +31: four chunks of 16 codes a thread; the
+            // 64-column atom w & 3, rows 16 (w >> 2) .. +15: two chunks of 16 codes a thread; the
             // rows of a phase (r and r + 4) meet no bank twice, loading or storing
-            const int atom = w & 3, row0 = (w >> 2) * 32 + (lane >> 3) + ((lane >> 2) & 1) * 4;
+            const int atom = w & 3, row0 = (w >> 2) * 16 + (lane >> 3) + ((lane >> 2) & 1) * 4;
             const int unit = (atom & 1) * 4 + (lane & 3), bunit = 2 * (lane & 3), swap = (lane >> 2) & 1;
             const int64_t k = n0 + atom * 64;
             const float* sc = k < p.K ? p.q_scale + (k >> p.g_shift) * c.M : nullptr;
             // a step's tokens are read two steps ahead, their scales one
-            float next[4];
-            int tok[4];
+            float next[2];
+            int tok[2];
             auto load_tokens = [&](int it) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < 2; ++e) {
                     const int row = row0 + 8 * e;
                     tok[e] = it < n_st && sc && row < rows_of(it) ? c.plan.perm[seg0 + (rank + it * z) * 64 + row] : -1;
                 }
             };
             auto load_scales = [&]() {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+                for (int e = 0; e < 2; ++e)
                     next[e] = tok[e] >= 0 ? __ldg(sc + tok[e]) : 0.f;
             };
             load_tokens(0);
             load_scales();
             load_tokens(1);
             for (int it = 0; it < n_st; ++it) {
-                float s[4];
+                float s[2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+                for (int e = 0; e < 2; ++e)
                     s[e] = next[e];
                 load_scales();
                 load_tokens(it + 2);
@@ -1135,12 +1135,12 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
                 }
                 const uint8_t* raw = S(slot) + (atom >> 1) * kAtom;
                 const uint32_t dst = smem_u32(D(b)) + atom * kAtom;
-                uint4 v[4];
+                uint4 v[2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+                for (int e = 0; e < 2; ++e)
                     v[e] = *reinterpret_cast<const uint4*>(raw + swz128(row0 + 8 * e, unit));
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < 2; ++e) {
                     const uint32_t cw[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
                     uint32_t o[8];
 #pragma unroll
@@ -1186,10 +1186,10 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
             abort_flag = 1;
         const bool sums = n_st > 0 && mbar_wait_bounded(&acc_full, 0, c.status) && !aborted(&abort_flag);
         tc_fence_after();
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        const int pitch = c.Rq + 4, sub = w >> 2, q = warp & 3;
+        asm volatile("bar.sync 1, %0;" ::"n"(kGramWork * 32) : "memory");
+        const int pitch = c.Rq + 4, sub = (w >> 2) & 1, q = warp & 3;  // two warps for 32 rows, 16 columns each in turn
         float* red = reinterpret_cast<float*>(smem) + (size_t)(sub * 128 + 32 * q + lane) * pitch;
-        for (int col = 0; col < c.Rq; col += 16) {
+        for (int col = 16 * (w >> 3); col < c.Rq; col += 32) {
             uint32_t r[16];
             if (sums) {
                 tmem_ld16(tmem + (uint32_t)(sub * c.Rq + col) + ((uint32_t)(32 * q) << 16), r);

@@ -62,14 +62,14 @@ __global__ void __launch_bounds__(256) dequantize_int8_groups_kernel(const int8_
 //                 boxes {128 bytes, 64 tokens}
 //   warp 1        512 columns of tensor memory; one thread issues M = 128, N = 256, K = 16 MMAs, MT
 //                 of them on each decoded B step
-//   warps 2..9    decode: 16 codes (one 16-byte load) -> s q in fp32, rounded once to the operand
+//   warps 2..17   decode: 16 codes (one 16-byte load) -> s q in fp32, rounded once to the operand
 //                 type, two 16-byte swizzled stores.  Eight lanes of a load or store phase cover
 //                 rows r and r + 4 of one 64-input atom, which meet no bank twice
-//   warps 10..    epilogue: 32 rows n each, 16-byte stores of dW
+//   warps 18..    epilogue: 32 rows n each, 16-byte stores of dW
 // MT = 2 (two accumulators on one decoded step) halves the decode work and the code bytes per
 // product; MT = 1 keeps two accumulators in turn, so that a tile is written while the next one is
 // multiplied.
-constexpr int kXWarps = 8;
+constexpr int kXWarps = 16;   // 8 took 1.2 us to decode a stage, its MMAs 0.76
 constexpr int kKT = 256;      // inputs k of a tile
 constexpr int kStageM = 64;   // tokens of a stage
 
@@ -139,7 +139,7 @@ QLIN_DEV void wg_tile(int t, int tiles_n, int tiles_k, int& nt, int& kt)
     kt = r / gn;
 }
 
-template <int MT>
+template <int MT, int F16>
 __global__ void __launch_bounds__(WgCfg<MT>::THREADS, 1) wgrad_tc_kernel(const __grid_constant__ WgParams p)
 {
     using C = WgCfg<MT>;
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(WgCfg<MT>::THREADS, 1) wgrad_tc_kernel(const _
     } else if (warp == 1) {
         if (lane == 0) {
             // D f32; A, B of one 16-bit type (bf16 = 1), both MN-major; N = 256, M = 128
-            const uint32_t ty = p.f16 ? 0u : (1u << 7) | (1u << 10);
+            const uint32_t ty = F16 ? 0u : (1u << 7) | (1u << 10);
             const uint32_t idesc =
                 (1u << 4) | ty | (1u << 15) | (1u << 16) | ((uint32_t)(kKT >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
             constexpr uint32_t ATOM = 128 * kStageM;
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(WgCfg<MT>::THREADS, 1) wgrad_tc_kernel(const _
         __syncwarp();
     } else if (warp < 2 + kXWarps) {
         const int w = warp - 2, atom = w & 3;
-        const int row0 = (w >> 2) * 32 + (lane >> 3) + ((lane >> 2) & 1) * 4;  // + 8 j, j = 0 .. 3
+        const int row0 = (w >> 2) * 16 + (lane >> 3) + ((lane >> 2) & 1) * 4;  // + 8 j, j = 0, 1
         const int unit = (atom & 1) * 4 + (lane & 3), bunit = 2 * (lane & 3), swap = (lane >> 2) & 1;
         int it = 0;
         bool ok = true;
@@ -264,10 +264,10 @@ __global__ void __launch_bounds__(WgCfg<MT>::THREADS, 1) wgrad_tc_kernel(const _
             wg_tile((int)blockIdx.x + ti * (int)gridDim.x, p.tiles_n, p.tiles_k, nt, kt);
             const int64_t k = (int64_t)kt * kKT + atom * 64;
             const float* sc = k < p.K ? p.scale + (k >> p.g_shift) * p.M : nullptr;
-            float s[4], next[4];
-            auto load_scales = [&](int mb, float (&d)[4]) {
+            float s[2], next[2];
+            auto load_scales = [&](int mb, float (&d)[2]) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < 2; ++j) {
                     const int64_t m = (int64_t)mb * kStageM + row0 + 8 * j;
                     d[j] = sc && m < p.M ? __ldg(sc + m) : 0.f;
                 }
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(WgCfg<MT>::THREADS, 1) wgrad_tc_kernel(const _
             load_scales(0, next);
             for (int mb = 0; mb < nm; ++mb, ++it) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < 2; ++j)
                     s[j] = next[j];
                 if (mb + 1 < nm)
                     load_scales(mb + 1, next);
@@ -288,20 +288,20 @@ __global__ void __launch_bounds__(WgCfg<MT>::THREADS, 1) wgrad_tc_kernel(const _
                 }
                 const uint32_t raw = smem_u32(RAW(slot)) + (atom >> 1) * 128 * kStageM;
                 const uint32_t dst = smem_u32(BT(b)) + atom * 128 * kStageM;
-                uint4 v[4];
+                uint4 v[2];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < 2; ++j)
                     v[j] = ld_shared_v4(raw + swz128(row0 + 8 * j, unit));
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < 2; ++j) {
                     const int row = row0 + 8 * j;
                     const uint32_t c[4] = {v[j].x ^ 0x80808080u, v[j].y ^ 0x80808080u, v[j].z ^ 0x80808080u,
                                            v[j].w ^ 0x80808080u};
                     uint32_t h[8];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        h[2 * e] = pack_h16x2(code_f32(c[e], 0) * s[j], code_f32(c[e], 1) * s[j], p.f16);
-                        h[2 * e + 1] = pack_h16x2(code_f32(c[e], 2) * s[j], code_f32(c[e], 3) * s[j], p.f16);
+                        h[2 * e] = pack_h16x2(code_f32(c[e], 0) * s[j], code_f32(c[e], 1) * s[j], F16);
+                        h[2 * e + 1] = pack_h16x2(code_f32(c[e], 2) * s[j], code_f32(c[e], 3) * s[j], F16);
                     }
                     // rows r + 4 of a phase store their second half first
                     const uint32_t first = dst + swz128(row, bunit + swap), second = dst + swz128(row, bunit + 1 - swap);
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(WgCfg<MT>::THREADS, 1) wgrad_tc_kernel(const _
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             w[e] = pack_h16x2(__uint_as_float(r[h >> 1][(h & 1) * 8 + 2 * e]),
-                                              __uint_as_float(r[h >> 1][(h & 1) * 8 + 2 * e + 1]), p.f16);
+                                              __uint_as_float(r[h >> 1][(h & 1) * 8 + 2 * e + 1]), F16);
                         *reinterpret_cast<uint4*>(o + c + 8 * h) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
@@ -405,7 +405,7 @@ template <int MT>
 cudaError_t launch_wgrad(WgParams& p, cudaStream_t st, const DeviceInfo& dev)
 {
     using C = WgCfg<MT>;
-    auto kern = wgrad_tc_kernel<MT>;
+    auto kern = p.f16 ? wgrad_tc_kernel<MT, 1> : wgrad_tc_kernel<MT, 0>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess)
         return e;
