@@ -54,46 +54,55 @@ __global__ void __launch_bounds__(256) dequantize_int8_groups_kernel(const int8_
 
 // ------------------------------------------------------------------------------------ wgrad
 //
-// A persistent, warp-specialised tcgen05 GEMM over tiles of 128 MT outputs n by 256 inputs k.  The
-// contraction runs over tokens, the slow dimension of both operands in memory, so both are read
-// MN-major (a shared-memory row holds one token's 64 outputs or inputs, 128 bytes, 128-byte
-// swizzle) and nothing is transposed:
+// A persistent, warp-specialised tcgen05 GEMM.  The contraction runs over tokens, the slow
+// dimension of both operands in memory, so both are read MN-major (a shared-memory row holds one
+// token's 64 outputs or inputs, 128 bytes, 128-byte swizzle) and nothing is transposed.  Shared
+// memory bounds it: the MMAs' operand reads, the decoded codes and the copies all pass through its
+// 128 bytes a clock.  So two CTAs work as a pair on tiles of 512 outputs n by 256 inputs k: each
+// holds its own 256 outputs of dy and half of the decoded inputs, which the pair's MMAs (M = 256,
+// N = 256) share -- 128 KB of traffic a stage of 64 tokens instead of the 192 KB that one CTA needs
+// for a 256 x 256 tile.  Few tokens leave the writing of dW as the bound: then single CTAs take
+// tiles of 128 x 256 with two accumulators in turn, and write one while the next is multiplied.
 //   warp 0        TMA producer: dy boxes {64 outputs, 64 tokens}, the A operand as it is, and code
 //                 boxes {128 bytes, 64 tokens}
-//   warp 1        512 columns of tensor memory; one thread issues M = 128, N = 256, K = 16 MMAs, MT
-//                 of them on each decoded B step
-//   warps 2..17   decode: 16 codes (one 16-byte load) -> s q in fp32, rounded once to the operand
+//   warp 1        512 columns of tensor memory; one thread (of the pair: in CTA 0) issues the MMAs,
+//                 two of them (the pair) on each decoded K = 16 step
+//   warps 2..     decode: 16 codes (one 16-byte load) -> s q in fp32, rounded once to the operand
 //                 type, two 16-byte swizzled stores.  Eight lanes of a load or store phase cover
-//                 rows r and r + 4 of one 64-input atom, which meet no bank twice
-//   warps 18..    epilogue: 32 rows n each, 16-byte stores of dW
-// MT = 2 (two accumulators on one decoded step) halves the decode work and the code bytes per
-// product; MT = 1 keeps two accumulators in turn, so that a tile is written while the next one is
-// multiplied.
-constexpr int kXWarps = 16;   // 8 took 1.2 us to decode a stage, its MMAs 0.76
+//                 rows r and r + 4 of one 64-input atom, which meet no bank twice.  In the first
+//                 column of tiles they also add up dy's columns: db
+//   then          epilogue: 32 rows n each, 16-byte stores of dW
+// Every wait is bounded; on expiry the kernel records the timeout, every role stops, and TMEM is
+// freed once the MMAs in flight are done.
 constexpr int kKT = 256;      // inputs k of a tile
 constexpr int kStageM = 64;   // tokens of a stage
+constexpr uint32_t kAtomBytes = 128 * kStageM;
 
-__host__ __device__ constexpr int cmin(int a, int b) { return a < b ? a : b; }
-
-template <int MT>
+template <bool PAIR>
 struct WgCfg {
-    static constexpr int TN = 128 * MT;
-    static constexpr int A_BYTES = TN * kStageM * 2;
-    static constexpr int RAW_BYTES = kKT * kStageM;
-    static constexpr int B_BYTES = kKT * kStageM * 2;
+    static constexpr int CTAS = PAIR ? 2 : 1;
+    static constexpr int SUBS = PAIR ? 2 : 1;     // accumulators of a tile: 128 outputs a CTA each
+    static constexpr int BUFS = PAIR ? 1 : 2;     // tiles held in tensor memory
+    static constexpr int CN = 128 * SUBS;         // outputs of a CTA
+    static constexpr int TN = CN * CTAS;          // outputs of a tile
+    static constexpr int CK = kKT / CTAS;         // inputs that a CTA decodes
+    static constexpr int XW = PAIR ? 8 : 16;      // decoding warps: two chunks a thread
+    static constexpr int EW = 4 * SUBS;
+    static constexpr int A_BYTES = CN * kStageM * 2;
+    static constexpr int RAW_BYTES = CK * kStageM;
+    static constexpr int B_BYTES = CK * kStageM * 2;
     static constexpr int SLOT = A_BYTES + RAW_BYTES;
-    static constexpr int NB = 2;
-    static constexpr int NS = cmin(4, (225 * 1024 - NB * B_BYTES) / SLOT);
-    static constexpr int BUFS = MT == 2 ? 1 : 2;
-    static constexpr int EW = 4 * MT;
-    static constexpr int THREADS = (2 + kXWarps + EW) * 32;
+    static constexpr int NB = PAIR ? 3 : 2;
+    static constexpr int NS = PAIR ? 4 : 4;
+    static constexpr int THREADS = (2 + XW + EW) * 32;
     struct Bars {
-        uint64_t full[NS], empty[NS], bfull[NB], bempty[NB], acc_full[2], acc_empty[2], mma_done;
+        uint64_t full[NS], empty[NS], bfull[NB], bempty[NB], acc_full[2], acc_empty[2], mma_done, sums;
         uint32_t tmem;
         int abort_flag;
+        float colsum[2][1024];  // [GROUPS][CN], two tiles' in turn
     };
     static constexpr int SMEM = NS * SLOT + NB * B_BYTES + (int)sizeof(Bars) + 1024;
-    static_assert(SMEM <= 227 * 1024 && NS >= 3, "shared memory");
+    static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
 struct WgParams {
@@ -101,6 +110,7 @@ struct WgParams {
     CUtensorMap tm_q;   // [M][K] bytes, box {128, 64}, 128-byte swizzle
     const float* scale; // [K/g][M]
     void* dw;           // [N][K]
+    void* db;           // [N] or null
     int64_t M, N, K;
     int g_shift;
     int tiles_n, tiles_k;
@@ -130,6 +140,65 @@ QLIN_DEV float code_f32(uint32_t u, int i)
     return __uint_as_float(prmt(u, 0x4B000000u, 0x7650u + (uint32_t)i)) - 8388736.f;
 }
 
+// ---- the pair: CTA 0 of a cluster of two leads
+QLIN_DEV void pair_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Arrives on CTA 0's barrier at this address.  What the arrival announces was written in this CTA's
+// own shared memory and shown to the async proxy by the fence before it, so it needs no release at
+// cluster scope (which took 1300 cycles for each stage).
+QLIN_DEV void arrive_leader(uint64_t* bar)
+{
+    asm volatile(
+        "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\t"
+        "mbarrier.arrive.shared::cluster.b64 _, [r];\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
+}
+template <bool PAIR>
+QLIN_DEV void wg_alloc(uint32_t* dst)
+{
+    if constexpr (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(dst)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        tmem_alloc(dst, 512);
+    }
+}
+template <bool PAIR>
+QLIN_DEV void wg_dealloc(uint32_t base)
+{
+    if constexpr (PAIR)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(base) : "memory");
+    else
+        tmem_dealloc(base, 512);
+}
+template <bool PAIR>
+QLIN_DEV void wg_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        tc_mma<false>(d, a, b, idesc, accumulate);
+}
+// Arrives on bar (of the pair: in both CTAs) once every MMA issued so far is done.
+template <bool PAIR>
+QLIN_DEV void wg_commit(uint64_t* bar)
+{
+    if constexpr (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                smem_u32(bar)),
+            "h"((uint16_t)3)
+            : "memory");
+    else
+        tc_commit(bar);
+}
+
 // Groups of 8 tiles along n walk the k tiles together: their dy columns and the codes stay in L2.
 QLIN_DEV void wg_tile(int t, int tiles_n, int tiles_k, int& nt, int& kt)
 {
@@ -139,10 +208,10 @@ QLIN_DEV void wg_tile(int t, int tiles_n, int tiles_k, int& nt, int& kt)
     kt = r / gn;
 }
 
-template <int MT, int F16>
-__global__ void __launch_bounds__(WgCfg<MT>::THREADS, 1) wgrad_tc_kernel(const __grid_constant__ WgParams p)
+template <bool PAIR, int F16>
+__global__ void __launch_bounds__(WgCfg<PAIR>::THREADS, 1) wgrad_tc_kernel(const __grid_constant__ WgParams p)
 {
-    using C = WgCfg<MT>;
+    using C = WgCfg<PAIR>;
     using Bars = typename C::Bars;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -151,9 +220,11 @@ __global__ void __launch_bounds__(WgCfg<MT>::THREADS, 1) wgrad_tc_kernel(const _
     auto RAW = [&](int s) { return smem + s * C::SLOT + C::A_BYTES; };
     auto BT = [&](int b) { return smem + C::NS * C::SLOT + b * C::B_BYTES; };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = PAIR ? (int)(blockIdx.x & 1) : 0;
+    const int unit0 = (int)blockIdx.x / C::CTAS, units = (int)gridDim.x / C::CTAS;
     const int nm = (int)((p.M + kStageM - 1) / kStageM);
     const int tiles = p.tiles_n * p.tiles_k;
-    const int my_tiles = tiles > (int)blockIdx.x ? (tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+    const int my_tiles = tiles > unit0 ? (tiles - 1 - unit0) / units + 1 : 0;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::NS; ++s) {
@@ -161,19 +232,23 @@ __global__ void __launch_bounds__(WgCfg<MT>::THREADS, 1) wgrad_tc_kernel(const _
             mbar_init(&bars.empty[s], 1);
         }
         for (int b = 0; b < C::NB; ++b) {
-            mbar_init(&bars.bfull[b], kXWarps);
+            mbar_init(&bars.bfull[b], C::XW * C::CTAS);
             mbar_init(&bars.bempty[b], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&bars.acc_full[b], 1);
-            mbar_init(&bars.acc_empty[b], C::EW);
+            mbar_init(&bars.acc_empty[b], C::EW * C::CTAS);
         }
         mbar_init(&bars.mma_done, 1);
+        mbar_init(&bars.sums, C::XW);
         bars.abort_flag = 0;
         fence_mbar_init();
     }
+    __syncthreads();
+    if constexpr (PAIR)
+        pair_sync();  // both CTAs' barriers exist, both run
     if (warp == 1)
-        tmem_alloc(&bars.tmem, 512);
+        wg_alloc<PAIR>(&bars.tmem);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -186,7 +261,7 @@ __global__ void __launch_bounds__(WgCfg<MT>::THREADS, 1) wgrad_tc_kernel(const _
             bool ok = true;
             for (int ti = 0; ti < my_tiles && ok; ++ti) {
                 int nt, kt;
-                wg_tile((int)blockIdx.x + ti * (int)gridDim.x, p.tiles_n, p.tiles_k, nt, kt);
+                wg_tile(unit0 + ti * units, p.tiles_n, p.tiles_k, nt, kt);
                 for (int mb = 0; mb < nm; ++mb, ++it) {
                     const int slot = it % C::NS;
                     if ((it >= C::NS &&
@@ -198,12 +273,12 @@ __global__ void __launch_bounds__(WgCfg<MT>::THREADS, 1) wgrad_tc_kernel(const _
                     }
                     mbar_arrive_expect_tx(&bars.full[slot], C::SLOT);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        tma_load_2d(RAW(slot) + h * 128 * kStageM, &p.tm_q, kt * kKT + h * 128, mb * kStageM,
+                    for (int h = 0; h < C::CK / 128; ++h)
+                        tma_load_2d(RAW(slot) + h * kAtomBytes, &p.tm_q, kt * kKT + rank * C::CK + h * 128, mb * kStageM,
                                     &bars.full[slot]);
 #pragma unroll
-                    for (int a = 0; a < 2 * MT; ++a)
-                        tma_load_2d(A(slot) + a * 128 * kStageM, &p.tm_dy, nt * C::TN + a * 64, mb * kStageM,
+                    for (int a = 0; a < C::CN / 64; ++a)
+                        tma_load_2d(A(slot) + a * kAtomBytes, &p.tm_dy, nt * C::TN + rank * C::CN + a * 64, mb * kStageM,
                                     &bars.full[slot]);
                 }
             }
@@ -212,12 +287,11 @@ __global__ void __launch_bounds__(WgCfg<MT>::THREADS, 1) wgrad_tc_kernel(const _
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            // D f32; A, B of one 16-bit type (bf16 = 1), both MN-major; N = 256, M = 128
+        if (lane == 0 && rank == 0) {
+            // D f32; A, B of one 16-bit type (bf16 = 1), both MN-major; N = 256, M = 128 a CTA
             const uint32_t ty = F16 ? 0u : (1u << 7) | (1u << 10);
-            const uint32_t idesc =
-                (1u << 4) | ty | (1u << 15) | (1u << 16) | ((uint32_t)(kKT >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-            constexpr uint32_t ATOM = 128 * kStageM;
+            const uint32_t idesc = (1u << 4) | ty | (1u << 15) | (1u << 16) | ((uint32_t)(kKT >> 3) << 17) |
+                                   ((uint32_t)(128 * C::CTAS >> 4) << 24);
             int it = 0;
             bool ok = true;
             for (int ti = 0; ti < my_tiles && ok; ++ti) {
@@ -227,6 +301,7 @@ __global__ void __launch_bounds__(WgCfg<MT>::THREADS, 1) wgrad_tc_kernel(const _
                 const uint32_t acc = tmem + (uint32_t)(buf * 256);
                 for (int mb = 0; mb < nm && ok; ++mb, ++it) {
                     const int slot = it % C::NS, b = it % C::NB;
+                    // every decoding warp (of both CTAs) has seen its stage land before it arrived here
                     ok = mbar_wait_bounded(&bars.full[slot], (it / C::NS) & 1, p.status) &&
                          mbar_wait_bounded(&bars.bfull[b], (it / C::NB) & 1, p.status);
                     if (!ok)
@@ -235,34 +310,41 @@ __global__ void __launch_bounds__(WgCfg<MT>::THREADS, 1) wgrad_tc_kernel(const _
                     const uint32_t a0 = smem_u32(A(slot)), b0 = smem_u32(BT(b));
 #pragma unroll
                     for (int kk = 0; kk < kStageM / 16; ++kk) {
-                        const uint64_t bd = umma_desc_sw128_mn(b0 + kk * 2048, ATOM);
+                        const uint64_t bd = umma_desc_sw128_mn(b0 + kk * 2048, kAtomBytes);
 #pragma unroll
-                        for (int m = 0; m < MT; ++m)
-                            tc_mma<false>(acc + (uint32_t)(m * 256),
-                                          umma_desc_sw128_mn(a0 + m * 2 * ATOM + kk * 2048, ATOM), bd, idesc,
-                                          (mb | kk) != 0 ? 1u : 0u);
+                        for (int m = 0; m < C::SUBS; ++m)
+                            wg_mma<PAIR>(acc + (uint32_t)(m * 256),
+                                         umma_desc_sw128_mn(a0 + m * 2 * kAtomBytes + kk * 2048, kAtomBytes), bd, idesc,
+                                         (mb | kk) != 0 ? 1u : 0u);
                     }
-                    tc_commit(&bars.empty[slot]);
-                    tc_commit(&bars.bempty[b]);
+                    wg_commit<PAIR>(&bars.empty[slot]);
+                    wg_commit<PAIR>(&bars.bempty[b]);
                 }
-                tc_commit(&bars.acc_full[buf]);
+                wg_commit<PAIR>(&bars.acc_full[buf]);
             }
             if (!ok)
                 bars.abort_flag = 1;
-            tc_commit(&bars.mma_done);  // every MMA issued has completed before TMEM is released
+            wg_commit<PAIR>(&bars.mma_done);  // every MMA issued has completed before TMEM is released
             mbar_wait_bounded(&bars.mma_done, 0, p.status);
         }
         __syncwarp();
-    } else if (warp < 2 + kXWarps) {
-        const int w = warp - 2, atom = w & 3;
-        const int row0 = (w >> 2) * 16 + (lane >> 3) + ((lane >> 2) & 1) * 4;  // + 8 j, j = 0, 1
+    } else if (warp < 2 + C::XW) {
+        constexpr int ATOMS = C::CK / 64, RW = C::XW / ATOMS, RPW = kStageM / RW;  // rows a warp: 16
+        static_assert(RPW == 16, "two chunks a thread");
+        const int w = warp - 2, atom = w % ATOMS;
+        const int row0 = (w / ATOMS) * RPW + (lane >> 3) + ((lane >> 2) & 1) * 4;  // + 8 j, j = 0, 1
         const int unit = (atom & 1) * 4 + (lane & 3), bunit = 2 * (lane & 3), swap = (lane >> 2) & 1;
-        int it = 0;
+        // column sums: a pair of columns and one of GROUPS parts of a stage's rows for each thread
+        constexpr int PAIRS = C::CN / 2, GROUPS = C::XW * 32 / PAIRS, GR = kStageM / GROUPS;
+        const int ct = (int)threadIdx.x - 64, cp = ct % PAIRS, cg = ct / PAIRS;
+        int it = 0, n_sums = 0;
         bool ok = true;
         for (int ti = 0; ti < my_tiles && ok; ++ti) {
             int nt, kt;
-            wg_tile((int)blockIdx.x + ti * (int)gridDim.x, p.tiles_n, p.tiles_k, nt, kt);
-            const int64_t k = (int64_t)kt * kKT + atom * 64;
+            wg_tile(unit0 + ti * units, p.tiles_n, p.tiles_k, nt, kt);
+            const bool sums = kt == 0 && p.db != nullptr;
+            float sum0 = 0.f, sum1 = 0.f;
+            const int64_t k = (int64_t)kt * kKT + rank * C::CK + atom * 64;
             const float* sc = k < p.K ? p.scale + (k >> p.g_shift) * p.M : nullptr;
             float s[2], next[2];
             auto load_scales = [&](int mb, float (&d)[2]) {
@@ -286,8 +368,8 @@ __global__ void __launch_bounds__(WgCfg<MT>::THREADS, 1) wgrad_tc_kernel(const _
                     ok = false;
                     break;
                 }
-                const uint32_t raw = smem_u32(RAW(slot)) + (atom >> 1) * 128 * kStageM;
-                const uint32_t dst = smem_u32(BT(b)) + atom * 128 * kStageM;
+                const uint32_t raw = smem_u32(RAW(slot)) + (atom >> 1) * kAtomBytes;
+                const uint32_t dst = smem_u32(BT(b)) + atom * kAtomBytes;
                 uint4 v[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
@@ -304,25 +386,62 @@ __global__ void __launch_bounds__(WgCfg<MT>::THREADS, 1) wgrad_tc_kernel(const _
                         h[2 * e + 1] = pack_h16x2(code_f32(c[e], 2) * s[j], code_f32(c[e], 3) * s[j], F16);
                     }
                     // rows r + 4 of a phase store their second half first
-                    const uint32_t first = dst + swz128(row, bunit + swap), second = dst + swz128(row, bunit + 1 - swap);
+                    const uint32_t lo = dst + swz128(row, bunit), hi = dst + swz128(row, bunit + 1);
                     if (swap) {
-                        st_shared_v4(first, h[4], h[5], h[6], h[7]);
-                        st_shared_v4(second, h[0], h[1], h[2], h[3]);
+                        st_shared_v4(hi, h[4], h[5], h[6], h[7]);
+                        st_shared_v4(lo, h[0], h[1], h[2], h[3]);
                     } else {
-                        st_shared_v4(first, h[0], h[1], h[2], h[3]);
-                        st_shared_v4(second, h[4], h[5], h[6], h[7]);
+                        st_shared_v4(lo, h[0], h[1], h[2], h[3]);
+                        st_shared_v4(hi, h[4], h[5], h[6], h[7]);
                     }
+                }
+                if (sums) {  // before the arrival below frees the stage
+                    const uint8_t* a = A(slot) + (cp >> 5) * kAtomBytes + (cp & 3) * 4;
+                    float p0 = 0.f, p1 = 0.f;
+#pragma unroll
+                    for (int r = 0; r < GR; ++r) {
+                        const int row = cg * GR + r;
+                        const uint32_t d = *reinterpret_cast<const uint32_t*>(a + swz128(row, (cp & 31) >> 2));
+                        p0 += h16_to_float(d, F16);
+                        p1 += h16_to_float(d >> 16, F16);
+                    }
+                    sum0 += p0;
+                    sum1 += p1;
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
+                if (lane == 0) {
+                    if constexpr (PAIR)
+                        arrive_leader(&bars.bfull[b]);
+                    else
+                        mbar_arrive(&bars.bfull[b]);
+                }
+            }
+            if (sums && ok) {
+                // two buffers: whoever writes one again has met every warp at the sums between
+                float* part = bars.colsum[n_sums & 1];
+                part[cg * C::CN + 2 * cp] = sum0;
+                part[cg * C::CN + 2 * cp + 1] = sum1;
+                __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(&bars.bfull[b]);
+                    mbar_arrive(&bars.sums);
+                ok = mbar_wait_bounded(&bars.sums, n_sums & 1, p.status);
+                ++n_sums;
+                for (int i = ct; i < C::CN && ok; i += C::XW * 32) {
+                    const int64_t n = (int64_t)nt * C::TN + rank * C::CN + i;
+                    float t = 0.f;
+#pragma unroll
+                    for (int g = 0; g < GROUPS; ++g)
+                        t += part[g * C::CN + i];
+                    if (n < p.N)
+                        static_cast<unsigned short*>(p.db)[n] = to_h16(t, F16);
+                }
             }
         }
         if (!ok)
             bars.abort_flag = 1;
     } else {
-        const int q = warp & 3, sub = (warp - 2 - kXWarps) >> 2;
+        const int q = warp & 3, sub = (warp - 2 - C::XW) >> 2;
         for (int ti = 0; ti < my_tiles; ++ti) {
             const int buf = ti % C::BUFS;
             if (!mbar_wait_bounded(&bars.acc_full[buf], (ti / C::BUFS) & 1, p.status) || aborted(&bars.abort_flag)) {
@@ -331,8 +450,8 @@ __global__ void __launch_bounds__(WgCfg<MT>::THREADS, 1) wgrad_tc_kernel(const _
             }
             tc_fence_after();
             int nt, kt;
-            wg_tile((int)blockIdx.x + ti * (int)gridDim.x, p.tiles_n, p.tiles_k, nt, kt);
-            const int64_t n = (int64_t)nt * C::TN + sub * 128 + 32 * q + lane;
+            wg_tile(unit0 + ti * units, p.tiles_n, p.tiles_k, nt, kt);
+            const int64_t n = (int64_t)nt * C::TN + rank * C::CN + sub * 128 + 32 * q + lane;
             const uint32_t acc = tmem + (uint32_t)((buf + sub) * 256) + ((uint32_t)(32 * q) << 16);
             unsigned short* o = static_cast<unsigned short*>(p.dw) + n * p.K + (int64_t)kt * kKT;
             const int cols = (int)(p.K - (int64_t)kt * kKT < kKT ? p.K - (int64_t)kt * kKT : kKT);  // K % 64 == 0
@@ -356,72 +475,49 @@ __global__ void __launch_bounds__(WgCfg<MT>::THREADS, 1) wgrad_tc_kernel(const _
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&bars.acc_empty[buf]);
+            if (lane == 0) {
+                if constexpr (PAIR)
+                    arrive_leader(&bars.acc_empty[buf]);
+                else
+                    mbar_arrive(&bars.acc_empty[buf]);
+            }
         }
     }
     tc_fence_before();
     __syncthreads();
+    if constexpr (PAIR)
+        pair_sync();  // the pair's MMAs read both CTAs' shared memory; arrivals reach CTA 0's
     if (warp == 1)
-        tmem_dealloc(tmem, 512);
-}
-
-template <typename T>
-__global__ void __launch_bounds__(256) column_sum_kernel(const T* __restrict__ dy, int64_t M, int64_t N,
-                                                         T* __restrict__ db)
-{
-    // 64 columns a CTA: 8 threads of 8 columns along a row, 32 rows at a time
-    __shared__ float part[32][64];
-    const int64_t n = (int64_t)blockIdx.x * 64 + (threadIdx.x & 7) * 8;
-    const int r = threadIdx.x >> 3;
-    float sum[8] = {};
-    if (n < N) {
-#pragma unroll 8
-        for (int64_t m = r; m < M; m += 32) {
-            const uint4 v = ldg_stream_v4(dy + m * N + n);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                sum[2 * e] += h16_to_float(w[e], !__is_same(T, __nv_bfloat16));
-                sum[2 * e + 1] += h16_to_float(w[e] >> 16, !__is_same(T, __nv_bfloat16));
-            }
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        part[r][(threadIdx.x & 7) * 8 + e] = sum[e];
-    __syncthreads();
-    if (threadIdx.x < 64 && (int64_t)blockIdx.x * 64 + threadIdx.x < N) {
-        float t = 0.f;
-        for (int i = 0; i < 32; ++i)
-            t += part[i][threadIdx.x];
-        db[(int64_t)blockIdx.x * 64 + threadIdx.x] = from_float<T>(t);
-    }
+        wg_dealloc<PAIR>(tmem);
 }
 
 int log2_of(int g) { return g == 64 ? 6 : g == 128 ? 7 : 8; }
 
-template <int MT>
+template <bool PAIR>
 cudaError_t launch_wgrad(WgParams& p, cudaStream_t st, const DeviceInfo& dev)
 {
-    using C = WgCfg<MT>;
-    auto kern = p.f16 ? wgrad_tc_kernel<MT, 1> : wgrad_tc_kernel<MT, 0>;
+    using C = WgCfg<PAIR>;
+    auto kern = p.f16 ? wgrad_tc_kernel<PAIR, 1> : wgrad_tc_kernel<PAIR, 0>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess)
         return e;
     p.tiles_n = (int)((p.N + C::TN - 1) / C::TN);
     p.tiles_k = (int)((p.K + kKT - 1) / kKT);
-    const int64_t tiles = (int64_t)p.tiles_n * p.tiles_k;
+    const int64_t tiles = (int64_t)p.tiles_n * p.tiles_k, most = dev.sm_count / C::CTAS;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles < dev.sm_count ? tiles : dev.sm_count));
+    cfg.gridDim = dim3((unsigned)(C::CTAS * (tiles < most ? tiles : most)));
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C::CTAS;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = PAIR ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
@@ -449,6 +545,7 @@ cudaError_t launch_pergroup_wgrad(const void* dy, qlin_dtype dt, int64_t M, int6
     WgParams p;
     p.scale = scale;
     p.dw = dw;
+    p.db = db;
     p.M = M;
     p.N = N;
     p.K = K;
@@ -460,17 +557,7 @@ cudaError_t launch_pergroup_wgrad(const void* dy, qlin_dtype dt, int64_t M, int6
         !encode_tmap_2d(&p.tm_q, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, (uint64_t)K, (uint64_t)M, (uint64_t)K, 128,
                         kStageM))
         return cudaErrorInvalidValue;
-    const bool two = N > 128 && M > 512;
-    const cudaError_t e = two ? launch_wgrad<2>(p, st, dev) : launch_wgrad<1>(p, st, dev);
-    if (e != cudaSuccess || !db)
-        return e;
-    const unsigned blocks = (unsigned)((N + 63) / 64);
-    if (dt == QLIN_BF16)
-        column_sum_kernel<<<blocks, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(dy), M, N,
-                                                  static_cast<__nv_bfloat16*>(db));
-    else
-        column_sum_kernel<<<blocks, 256, 0, st>>>(static_cast<const __half*>(dy), M, N, static_cast<__half*>(db));
-    return cudaGetLastError();
+    return M > 512 && N > 256 ? launch_wgrad<true>(p, st, dev) : launch_wgrad<false>(p, st, dev);
 }
 
 }  // namespace qlin
