@@ -71,7 +71,11 @@ __global__ void __launch_bounds__(256) dequantize_int8_groups_kernel(const int8_
 //                 type, two 16-byte swizzled stores.  Eight lanes of a load or store phase cover
 //                 rows r and r + 4 of one 64-input atom, which meet no bank twice.  In the first
 //                 column of tiles they also add up dy's columns: db
-//   then          epilogue: 32 rows n each, 16-byte stores of dW
+//   then          epilogue: 32 rows n each, 32 columns at a time through a staging buffer, so that a
+//                 store writes 64 bytes of 8 rows (rows straight from tensor memory, 16 bytes of 32
+//                 rows an instruction, took 10,000 cycles a tile)
+// Where the last round of tiles fills at most half of the pairs, its tiles are cut into their two
+// accumulators' halves, one for a pair.
 // Every wait is bounded; on expiry the kernel records the timeout, every role stops, and TMEM is
 // freed once the MMAs in flight are done.
 constexpr int kKT = 256;      // inputs k of a tile
@@ -93,15 +97,15 @@ struct WgCfg {
     static constexpr int B_BYTES = CK * kStageM * 2;
     static constexpr int SLOT = A_BYTES + RAW_BYTES;
     static constexpr int NB = PAIR ? 3 : 2;
-    static constexpr int NS = PAIR ? 4 : 4;
+    static constexpr int NS = 4;
+    static constexpr int STAGE_OUT = EW * 32 * 64;  // staging of the epilogue's warps
     static constexpr int THREADS = (2 + XW + EW) * 32;
     struct Bars {
-        uint64_t full[NS], empty[NS], bfull[NB], bempty[NB], acc_full[2], acc_empty[2], mma_done, sums;
+        uint64_t full[NS], empty[NS], bfull[NB], bempty[NB], acc_full[2], acc_empty[2], mma_done;
         uint32_t tmem;
         int abort_flag;
-        float colsum[2][1024];  // [GROUPS][CN], two tiles' in turn
     };
-    static constexpr int SMEM = NS * SLOT + NB * B_BYTES + (int)sizeof(Bars) + 1024;
+    static constexpr int SMEM = NS * SLOT + NB * B_BYTES + STAGE_OUT + (int)sizeof(Bars) + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -114,6 +118,7 @@ struct WgParams {
     int64_t M, N, K;
     int g_shift;
     int tiles_n, tiles_k;
+    int whole;          // tiles taken whole; later ones in halves
     int f16;
     unsigned* status;
 };
@@ -199,6 +204,11 @@ QLIN_DEV void wg_commit(uint64_t* bar)
         tc_commit(bar);
 }
 
+// One piece of work: a tile, all of its accumulators or one.
+struct WgUnit {
+    int nt, kt, sub, subs;
+};
+
 // Groups of 8 tiles along n walk the k tiles together: their dy columns and the codes stay in L2.
 QLIN_DEV void wg_tile(int t, int tiles_n, int tiles_k, int& nt, int& kt)
 {
@@ -208,6 +218,17 @@ QLIN_DEV void wg_tile(int t, int tiles_n, int tiles_k, int& nt, int& kt)
     kt = r / gn;
 }
 
+template <bool PAIR>
+QLIN_DEV WgUnit wg_unit(int u, const WgParams& p)
+{
+    WgUnit w;
+    const int cut = u - p.whole;
+    w.sub = PAIR && cut >= 0 ? cut & 1 : 0;
+    w.subs = PAIR && cut < 0 ? 2 : 1;
+    wg_tile(PAIR && cut >= 0 ? p.whole + (cut >> 1) : u, p.tiles_n, p.tiles_k, w.nt, w.kt);
+    return w;
+}
+
 template <bool PAIR, int F16>
 __global__ void __launch_bounds__(WgCfg<PAIR>::THREADS, 1) wgrad_tc_kernel(const __grid_constant__ WgParams p)
 {
@@ -215,7 +236,7 @@ __global__ void __launch_bounds__(WgCfg<PAIR>::THREADS, 1) wgrad_tc_kernel(const
     using Bars = typename C::Bars;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Bars& bars = *reinterpret_cast<Bars*>(smem + C::NS * C::SLOT + C::NB * C::B_BYTES);
+    Bars& bars = *reinterpret_cast<Bars*>(smem + C::NS * C::SLOT + C::NB * C::B_BYTES + C::STAGE_OUT);
     auto A = [&](int s) { return smem + s * C::SLOT; };
     auto RAW = [&](int s) { return smem + s * C::SLOT + C::A_BYTES; };
     auto BT = [&](int b) { return smem + C::NS * C::SLOT + b * C::B_BYTES; };
@@ -223,7 +244,7 @@ __global__ void __launch_bounds__(WgCfg<PAIR>::THREADS, 1) wgrad_tc_kernel(const
     const int rank = PAIR ? (int)(blockIdx.x & 1) : 0;
     const int unit0 = (int)blockIdx.x / C::CTAS, units = (int)gridDim.x / C::CTAS;
     const int nm = (int)((p.M + kStageM - 1) / kStageM);
-    const int tiles = p.tiles_n * p.tiles_k;
+    const int all = p.tiles_n * p.tiles_k, tiles = PAIR ? 2 * all - p.whole : all;
     const int my_tiles = tiles > unit0 ? (tiles - 1 - unit0) / units + 1 : 0;
 
     if (threadIdx.x == 0) {
@@ -240,7 +261,6 @@ __global__ void __launch_bounds__(WgCfg<PAIR>::THREADS, 1) wgrad_tc_kernel(const
             mbar_init(&bars.acc_empty[b], C::EW * C::CTAS);
         }
         mbar_init(&bars.mma_done, 1);
-        mbar_init(&bars.sums, C::XW);
         bars.abort_flag = 0;
         fence_mbar_init();
     }
@@ -260,8 +280,7 @@ __global__ void __launch_bounds__(WgCfg<PAIR>::THREADS, 1) wgrad_tc_kernel(const
             int it = 0;
             bool ok = true;
             for (int ti = 0; ti < my_tiles && ok; ++ti) {
-                int nt, kt;
-                wg_tile(unit0 + ti * units, p.tiles_n, p.tiles_k, nt, kt);
+                const WgUnit w = wg_unit<PAIR>(unit0 + ti * units, p);
                 for (int mb = 0; mb < nm; ++mb, ++it) {
                     const int slot = it % C::NS;
                     if ((it >= C::NS &&
@@ -271,14 +290,13 @@ __global__ void __launch_bounds__(WgCfg<PAIR>::THREADS, 1) wgrad_tc_kernel(const
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&bars.full[slot], C::SLOT);
+                    mbar_arrive_expect_tx(&bars.full[slot], (unsigned)(C::RAW_BYTES + w.subs * 2 * (int)kAtomBytes));
 #pragma unroll
                     for (int h = 0; h < C::CK / 128; ++h)
-                        tma_load_2d(RAW(slot) + h * kAtomBytes, &p.tm_q, kt * kKT + rank * C::CK + h * 128, mb * kStageM,
+                        tma_load_2d(RAW(slot) + h * kAtomBytes, &p.tm_q, w.kt * kKT + rank * C::CK + h * 128, mb * kStageM,
                                     &bars.full[slot]);
-#pragma unroll
-                    for (int a = 0; a < C::CN / 64; ++a)
-                        tma_load_2d(A(slot) + a * kAtomBytes, &p.tm_dy, nt * C::TN + rank * C::CN + a * 64, mb * kStageM,
+                    for (int a = 2 * w.sub; a < 2 * (w.sub + w.subs); ++a)
+                        tma_load_2d(A(slot) + a * kAtomBytes, &p.tm_dy, w.nt * C::TN + rank * C::CN + a * 64, mb * kStageM,
                                     &bars.full[slot]);
                 }
             }
@@ -296,6 +314,7 @@ __global__ void __launch_bounds__(WgCfg<PAIR>::THREADS, 1) wgrad_tc_kernel(const
             bool ok = true;
             for (int ti = 0; ti < my_tiles && ok; ++ti) {
                 const int buf = ti % C::BUFS;
+                const WgUnit w = wg_unit<PAIR>(unit0 + ti * units, p);
                 ok = mbar_wait_bounded(&bars.acc_empty[buf], ((ti / C::BUFS) & 1) ^ 1, p.status);
                 tc_fence_after();
                 const uint32_t acc = tmem + (uint32_t)(buf * 256);
@@ -312,10 +331,13 @@ __global__ void __launch_bounds__(WgCfg<PAIR>::THREADS, 1) wgrad_tc_kernel(const
                     for (int kk = 0; kk < kStageM / 16; ++kk) {
                         const uint64_t bd = umma_desc_sw128_mn(b0 + kk * 2048, kAtomBytes);
 #pragma unroll
-                        for (int m = 0; m < C::SUBS; ++m)
+                        for (int m = 0; m < C::SUBS; ++m) {
+                            if (m < w.sub || m >= w.sub + w.subs)
+                                continue;
                             wg_mma<PAIR>(acc + (uint32_t)(m * 256),
                                          umma_desc_sw128_mn(a0 + m * 2 * kAtomBytes + kk * 2048, kAtomBytes), bd, idesc,
                                          (mb | kk) != 0 ? 1u : 0u);
+                        }
                     }
                     wg_commit<PAIR>(&bars.empty[slot]);
                     wg_commit<PAIR>(&bars.bempty[b]);
@@ -334,16 +356,15 @@ __global__ void __launch_bounds__(WgCfg<PAIR>::THREADS, 1) wgrad_tc_kernel(const
         const int w = warp - 2, atom = w % ATOMS;
         const int row0 = (w / ATOMS) * RPW + (lane >> 3) + ((lane >> 2) & 1) * 4;  // + 8 j, j = 0, 1
         const int unit = (atom & 1) * 4 + (lane & 3), bunit = 2 * (lane & 3), swap = (lane >> 2) & 1;
-        // column sums: a pair of columns and one of GROUPS parts of a stage's rows for each thread
-        constexpr int PAIRS = C::CN / 2, GROUPS = C::XW * 32 / PAIRS, GR = kStageM / GROUPS;
-        const int ct = (int)threadIdx.x - 64, cp = ct % PAIRS, cg = ct / PAIRS;
-        int it = 0, n_sums = 0;
+        const int ct = (int)threadIdx.x - 64;  // column sums: a column a thread
+        int it = 0;
         bool ok = true;
         for (int ti = 0; ti < my_tiles && ok; ++ti) {
-            int nt, kt;
-            wg_tile(unit0 + ti * units, p.tiles_n, p.tiles_k, nt, kt);
+            const WgUnit wu = wg_unit<PAIR>(unit0 + ti * units, p);
+            const int kt = wu.kt;
             const bool sums = kt == 0 && p.db != nullptr;
-            float sum0 = 0.f, sum1 = 0.f;
+            const bool here = ct >= 128 * wu.sub && ct < 128 * (wu.sub + wu.subs);  // this thread's column is loaded
+            float sum = 0.f;
             const int64_t k = (int64_t)kt * kKT + rank * C::CK + atom * 64;
             const float* sc = k < p.K ? p.scale + (k >> p.g_shift) * p.M : nullptr;
             float s[2], next[2];
@@ -395,18 +416,13 @@ __global__ void __launch_bounds__(WgCfg<PAIR>::THREADS, 1) wgrad_tc_kernel(const
                         st_shared_v4(hi, h[4], h[5], h[6], h[7]);
                     }
                 }
-                if (sums) {  // before the arrival below frees the stage
-                    const uint8_t* a = A(slot) + (cp >> 5) * kAtomBytes + (cp & 3) * 4;
-                    float p0 = 0.f, p1 = 0.f;
-#pragma unroll
-                    for (int r = 0; r < GR; ++r) {
-                        const int row = cg * GR + r;
-                        const uint32_t d = *reinterpret_cast<const uint32_t*>(a + swz128(row, (cp & 31) >> 2));
-                        p0 += h16_to_float(d, F16);
-                        p1 += h16_to_float(d >> 16, F16);
-                    }
-                    sum0 += p0;
-                    sum1 += p1;
+                if (sums && here) {  // before the arrival below frees the stage
+                    const uint8_t* a = A(slot) + (ct >> 6) * kAtomBytes + (ct & 7) * 2;
+                    float part = 0.f;
+#pragma unroll 16
+                    for (int row = 0; row < kStageM; ++row)
+                        part += h16_to_float(*reinterpret_cast<const unsigned short*>(a + swz128(row, (ct & 63) >> 3)), F16);
+                    sum += part;
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -417,31 +433,17 @@ __global__ void __launch_bounds__(WgCfg<PAIR>::THREADS, 1) wgrad_tc_kernel(const
                         mbar_arrive(&bars.bfull[b]);
                 }
             }
-            if (sums && ok) {
-                // two buffers: whoever writes one again has met every warp at the sums between
-                float* part = bars.colsum[n_sums & 1];
-                part[cg * C::CN + 2 * cp] = sum0;
-                part[cg * C::CN + 2 * cp + 1] = sum1;
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&bars.sums);
-                ok = mbar_wait_bounded(&bars.sums, n_sums & 1, p.status);
-                ++n_sums;
-                for (int i = ct; i < C::CN && ok; i += C::XW * 32) {
-                    const int64_t n = (int64_t)nt * C::TN + rank * C::CN + i;
-                    float t = 0.f;
-#pragma unroll
-                    for (int g = 0; g < GROUPS; ++g)
-                        t += part[g * C::CN + i];
-                    if (n < p.N)
-                        static_cast<unsigned short*>(p.db)[n] = to_h16(t, F16);
-                }
+            if (sums && here && ok) {
+                const int64_t n = (int64_t)wu.nt * C::TN + rank * C::CN + ct;
+                if (n < p.N)
+                    static_cast<unsigned short*>(p.db)[n] = to_h16(sum, F16);
             }
         }
         if (!ok)
             bars.abort_flag = 1;
     } else {
         const int q = warp & 3, sub = (warp - 2 - C::XW) >> 2;
+        const uint32_t out = smem_u32(smem + C::NS * C::SLOT + C::NB * C::B_BYTES) + (uint32_t)(warp - 2 - C::XW) * 2048u;
         for (int ti = 0; ti < my_tiles; ++ti) {
             const int buf = ti % C::BUFS;
             if (!mbar_wait_bounded(&bars.acc_full[buf], (ti / C::BUFS) & 1, p.status) || aborted(&bars.abort_flag)) {
@@ -449,28 +451,38 @@ __global__ void __launch_bounds__(WgCfg<PAIR>::THREADS, 1) wgrad_tc_kernel(const
                 break;
             }
             tc_fence_after();
-            int nt, kt;
-            wg_tile(unit0 + ti * units, p.tiles_n, p.tiles_k, nt, kt);
-            const int64_t n = (int64_t)nt * C::TN + rank * C::CN + sub * 128 + 32 * q + lane;
+            const WgUnit w = wg_unit<PAIR>(unit0 + ti * units, p);
             const uint32_t acc = tmem + (uint32_t)((buf + sub) * 256) + ((uint32_t)(32 * q) << 16);
-            unsigned short* o = static_cast<unsigned short*>(p.dw) + n * p.K + (int64_t)kt * kKT;
-            const int cols = (int)(p.K - (int64_t)kt * kKT < kKT ? p.K - (int64_t)kt * kKT : kKT);  // K % 64 == 0
+            const int64_t n_first = (int64_t)w.nt * C::TN + rank * C::CN + sub * 128 + 32 * q;
+            const int64_t k_first = (int64_t)w.kt * kKT;
+            const int cols = (int)(p.K - k_first < kKT ? p.K - k_first : kKT);  // K % 64 == 0
+            unsigned short* dw = static_cast<unsigned short*>(p.dw);
+            const bool mine = sub >= w.sub && sub < w.sub + w.subs;
 #pragma unroll 1
-            for (int c = 0; c < cols; c += 32) {
+            for (int c = 0; c < cols && mine; c += 32) {
                 uint32_t r[2][16];
                 tmem_ld16_nowait(acc + (uint32_t)c, r[0]);
                 tmem_ld16_nowait(acc + (uint32_t)c + 16u, r[1]);
                 tmem_wait_ld();
-                if (n < p.N) {
+                __syncwarp();  // the last 32 columns have been read
+                // staged rows of 64 bytes, 16-byte units permuted by row / 2: eight rows of a store or
+                // load phase meet no bank twice
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        uint32_t w[4];
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t o[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[e] = pack_h16x2(__uint_as_float(r[h >> 1][(h & 1) * 8 + 2 * e]),
-                                              __uint_as_float(r[h >> 1][(h & 1) * 8 + 2 * e + 1]), F16);
-                        *reinterpret_cast<uint4*>(o + c + 8 * h) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        o[e] = pack_h16x2(__uint_as_float(r[h >> 1][(h & 1) * 8 + 2 * e]),
+                                          __uint_as_float(r[h >> 1][(h & 1) * 8 + 2 * e + 1]), F16);
+                    st_shared_v4(out + lane * 64 + ((h ^ (lane >> 1) & 3) << 4), o[0], o[1], o[2], o[3]);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const int row = 8 * h + (lane >> 2);
+                    const uint4 v = ld_shared_v4(out + row * 64 + (((lane & 3) ^ (row >> 1) & 3) << 4));
+                    if (n_first + row < p.N)
+                        *reinterpret_cast<uint4*>(dw + (n_first + row) * p.K + k_first + c + 8 * (lane & 3)) = v;
                 }
             }
             tc_fence_before();
@@ -503,7 +515,11 @@ cudaError_t launch_wgrad(WgParams& p, cudaStream_t st, const DeviceInfo& dev)
         return e;
     p.tiles_n = (int)((p.N + C::TN - 1) / C::TN);
     p.tiles_k = (int)((p.K + kKT - 1) / kKT);
-    const int64_t tiles = (int64_t)p.tiles_n * p.tiles_k, most = dev.sm_count / C::CTAS;
+    const int64_t most = dev.sm_count / C::CTAS;
+    int64_t tiles = (int64_t)p.tiles_n * p.tiles_k;
+    const int64_t rest = tiles % most;
+    p.whole = (int)(PAIR && 2 * rest <= most ? tiles - rest : tiles);
+    tiles += tiles - p.whole;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(C::CTAS * (tiles < most ? tiles : most)));
     cfg.blockDim = dim3(C::THREADS);
