@@ -1368,12 +1368,14 @@ bool half_map(CUtensorMap& m, const Common& c, const uint16_t* p, uint32_t rows)
     return encode_tmap_2d(&m, tm_type<T>(), p, (uint64_t)c.Rq, (uint64_t)(2 * c.slots), (uint64_t)c.Rq * 2, 64, rows);
 }
 
-// CTAs that share a contraction of K: more until two an SM have work, at least four steps each.
-int narrow_split(const Common& c, int64_t K, const DeviceInfo& dev)
+// CTAs that share a contraction of K: as many as fit on the GPU in one round, at least four steps
+// each.  Three CTAs fit an SM, 54 a GPC, so 8 x 6 clusters of 8; two an SM (with rings of 110 KB) leave
+// room for 32, and 34 took a second round: dy [4096][14336] and its x, 137 us against 127.
+int narrow_split(const Common& c, int64_t K)
 {
     const int64_t tiles = max_tiles(c.M, c.L, kTileL), steps = (K + 63) / 64;
     int z = 1;
-    while (z < kMaxSplit && tiles * z < 2 * dev.sm_count && steps / (2 * z) >= 4)
+    while (z < kMaxSplit && tiles * 2 * z <= 384 && steps / (2 * z) >= 4)
         z *= 2;
     return z;
 }
@@ -1395,11 +1397,14 @@ cudaError_t launch_narrow(const Common& c, const void* w, int64_t K, const void*
         return cudaErrorInvalidValue;
     p.f_bytes = FWD ? c.Rq * 128 : (c.Rq + 63) / 64 * (int)kAtom;
     const int stage = 2 * (int)kAtom + p.f_bytes;
-    p.stages = 110 * 1024 / stage < kNarrowMaxStages ? 110 * 1024 / stage : kNarrowMaxStages;
+    const int z = narrow_split(c, K);
+    const int room = 74 * 1024;
+    p.stages = room / stage < kNarrowMaxStages ? room / stage : kNarrowMaxStages;
+    if (p.stages < 3)
+        p.stages = 3;
     const int red = 128 * (c.Rq + 4) * 4;
     const int smem = (p.stages * stage > red ? p.stages * stage : red) + 1024;
     p.tmem_cols = (int)tmem_columns(c.Rq);
-    const int z = narrow_split(c, K, dev);
     p.steps = (int)((K + 63) / 64 + z - 1) / z;
     const dim3 grid((unsigned)z, (unsigned)max_tiles(c.M, c.L, kTileL));
     return launch(adapters_narrow_kernel<T, FWD>, grid, kNarrowThreads, smem, z, p, st);
@@ -1444,7 +1449,7 @@ cudaError_t launch_grams(const Common& c, const AdapterBwdArgs& a, cudaStream_t 
     p.strips_x = (int)((a.K + 255) / 256);
     p.da = a.da;
     p.db = a.db;
-    p.parts = narrow_split(c, a.N, dev);
+    p.parts = narrow_split(c, a.N);
     p.tmem_cols = (int)tmem_columns(2 * c.Rq);
     if (!row_maps(p.dy, tm_type<T>(), 2, a.dy, c.M, a.N) ||
         !(a.q ? row_maps(p.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.q, c.M, a.K)
@@ -1504,7 +1509,7 @@ cudaError_t backward_t(const AdapterBwdArgs& a, cudaStream_t st, const DeviceInf
     const Common c = common_of(a.plan, a.dt, a.M, a.L, a.R, a.ws, dev);
     cudaError_t e = launch_narrow<T, false>(c, a.dy, a.N, a.b, a.scales, a.u, nullptr, st, dev);
     if (e == cudaSuccess && Is16<T>::f16) {
-        const SplitParams p = {c, a.u, narrow_split(c, a.N, dev)};
+        const SplitParams p = {c, a.u, narrow_split(c, a.N)};
         e = launch(adapters_split_kernel, dim3((unsigned)max_tiles(a.M, a.L, kTileL)), 256, 0, 0, p, st);
     }
     if (e == cudaSuccess)
