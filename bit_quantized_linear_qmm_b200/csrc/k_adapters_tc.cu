@@ -30,7 +30,7 @@ namespace qlin {
 namespace {
 
 constexpr uint32_t kAtom = 64 * 128;  // a 64-row x 128-byte swizzled block
-constexpr int kMaxSplit = 8;          // CTAs of a cluster: the portable size
+constexpr int kMaxSplit = 16;         // CTAs of a cluster (beyond 8: allowed on this GPU, not portable)
 
 // ------------------------------------------------------------------------------------ helpers
 
@@ -1231,12 +1231,12 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
                 if (z == 1) {
                     s = *reinterpret_cast<const float4*>(smem + (from - mine));
                 } else {
-                    float4 part[kMaxSplit];
+                    float4 part[8];
 #pragma unroll
-                    for (int k = 0; k < kMaxSplit; ++k)
+                    for (int k = 0; k < 8; ++k)
                         part[k] = k < z ? ld_peer_v4(peer_smem(from, (uint32_t)k)) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                    for (int k = 0; k < kMaxSplit; ++k) {
+                    for (int k = 0; k < 8; ++k) {
                         s.x += part[k].x;
                         s.y += part[k].y;
                         s.z += part[k].z;
@@ -1334,6 +1334,11 @@ cudaError_t launch(void (*kern)(const P), dim3 grid, int threads, int smem, int 
         if (e != cudaSuccess)
             return e;
     }
+    if (cluster_x > 8) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess)
+            return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
@@ -1370,12 +1375,13 @@ bool half_map(CUtensorMap& m, const Common& c, const uint16_t* p, uint32_t rows)
 
 // CTAs that share a contraction of K: as many as fit on the GPU in one round, at least four steps
 // each.  Three CTAs fit an SM, 54 a GPC, so 8 x 6 clusters of 8; two an SM (with rings of 110 KB) leave
-// room for 32, and 34 took a second round: dy [4096][14336] and its x, 137 us against 127.
+// room for 32, and 34 took a second round: dy [4096][14336] and its x, 137 us against 127.  A CTA's
+// boxes of 128-byte rows come at 33 GB/s at most, so few tiles are split over up to 16 CTAs.
 int narrow_split(const Common& c, int64_t K)
 {
     const int64_t tiles = max_tiles(c.M, c.L, kTileL), steps = (K + 63) / 64;
     int z = 1;
-    while (z < kMaxSplit && tiles * 2 * z <= 384 && steps / (2 * z) >= 4)
+    while (z < kMaxSplit && tiles * 2 * z <= (z < 8 ? 384 : 320) && steps / (2 * z) >= 4)
         z *= 2;
     return z;
 }
@@ -1460,7 +1466,7 @@ cudaError_t launch_grams(const Common& c, const AdapterBwdArgs& a, cudaStream_t 
     const int64_t jobs = (int64_t)c.L * (p.strips_y + p.strips_x);
     // split an adapter's tokens until every SM has work, at least two steps each on average
     int z = 1;
-    while (z < kMaxSplit && jobs * z < dev.sm_count && c.M / c.L / 64 >= 4 * z)
+    while (z < 8 && jobs * z < dev.sm_count && c.M / c.L / 64 >= 4 * z)
         z *= 2;
     return launch(adapters_gram_kernel<T>, dim3((unsigned)z, (unsigned)jobs), kGramThreads, p.room + 1024, z, p, st);
 }
