@@ -53,6 +53,12 @@ QLIN_DEV float4 ld_peer_v4(uint32_t addr)
                  : "r"(addr));
     return v;
 }
+QLIN_DEV float ld_peer(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
+}
 QLIN_DEV void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -945,18 +951,21 @@ __global__ void __launch_bounds__(kDecodeWarps * 32) adapters_decode_kernel(cons
 
 // ------------------------------------------------------------------------------------ grams
 
-// One cluster for each adapter and strip of 256 columns of dy or x: D[256][Rq] = S^T H over the
-// adapter's tokens, 64 at a time, the steps dealt round the cluster's CTAs.  S (dy, x or the
+// One cluster for each adapter and strip of 256 columns of dy or x: D = H^T S over the adapter's tokens, 64 at a time, the steps dealt round the cluster's CTAs.  S (dy, x or the
 // restored x) and H (the halves of u or v) lie token by token in shared memory, which is MN-major
 // for both operands; nothing is transposed.
 //   warps 0..3   the loads: S in 64-column boxes or gathers (codes: 128-byte ones), H in 64-rank boxes
-//   warp 4       tensor memory, the MMAs (two of M = 128 for hi and for lo, N = Rq, K = 16)
+//   warp 4       tensor memory, the MMAs (M = 128 ranks, N = 256 columns, K = 16).  Up to rank 64 the
+//                128 rows are the 64 of hi and the 64 of lo, added at the end: one MMA a step of 16
+//                (columns as M and ranks as N took four, each no faster)
 //   warps 5..20  codes: s q in fp32, rounded once to the operand type, into a ring of two buffers;
 //                rows past the adapter's last token: zeros (only there, so what another adapter's
 //                row holds enters no sum); then the epilogue
 constexpr int kGramWork = 16;  // 8 took 1950 cycles to decode a step, twice what its loads take
 constexpr int kGramThreads = (kLoadWarps + 1 + kGramWork) * 32;
 constexpr int kGramMaxStages = 6;
+constexpr int kGramPitch = 257;
+constexpr int kMaxGramSplit = 8;
 
 struct GramParams {
     RowMaps dy, x;         // x: 16-bit, or the codes
@@ -1014,6 +1023,7 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
     const int seg0 = c.plan.seg[i], tokens = c.plan.seg[i + 1] - seg0, tile0 = c.plan.tile_l0[i];
     const int steps = (tokens + 63) / 64;
     const int n_st = steps > rank ? (steps - 1 - rank) / z + 1 : 0;  // steps rank, rank + z, ...
+    const bool stacked = c.Rq <= 64;  // hi and lo are the two 64-rank atoms of one operand
     const int h_half = (c.Rq + 63) / 64 * (int)kAtom;
     const int src_bytes = of_q ? 2 * (int)kAtom : 4 * (int)kAtom, stage_bytes = src_bytes + 2 * h_half;
     const int ring = of_q ? 2 * 4 * (int)kAtom : 0;  // decoded buffers, first in shared memory
@@ -1059,8 +1069,9 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
     } else if (warp == kLoadWarps) {
         if (lane == 0) {
             const uint32_t ty = f16 ? 0u : (1u << 7) | (1u << 10);
-            const uint32_t idesc = (1u << 4) | ty | (1u << 15) | (1u << 16) | ((uint32_t)(c.Rq >> 3) << 17) |
-                                   ((uint32_t)(128 >> 4) << 24);
+            const uint32_t idesc =
+                (1u << 4) | ty | (1u << 15) | (1u << 16) | ((uint32_t)(256 >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+            const int halves = stacked ? 1 : 2;
             bool ok = true;
             for (int it = 0; it < n_st && ok; ++it) {
                 const int slot = it % stages, b = it & 1;
@@ -1074,14 +1085,9 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
                 const uint32_t a = smem_u32(of_q ? D(b) : S(slot)), h = smem_u32(H(slot));
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-                    for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-                        for (int half = 0; half < 2; ++half)
-                            tc_mma<false>(tmem + (uint32_t)(sub * c.Rq),
-                                          umma_desc_sw128_mn(a + sub * 2 * kAtom + kk * 2048, kAtom),
-                                          umma_desc_sw128_mn(h + half * h_half + kk * 2048, kAtom), idesc,
-                                          (it | kk | half) != 0 ? 1u : 0u);
+                    for (int half = 0; half < halves; ++half)
+                        tc_mma<false>(tmem, umma_desc_sw128_mn(h + half * h_half + kk * 2048, kAtom),
+                                      umma_desc_sw128_mn(a + kk * 2048, kAtom), idesc, (it | kk | half) != 0 ? 1u : 0u);
                 tc_commit(&empty[slot]);
                 if (of_q)
                     tc_commit(&taken[b]);
@@ -1187,20 +1193,25 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
         const bool sums = n_st > 0 && mbar_wait_bounded(&acc_full, 0, c.status) && !aborted(&abort_flag);
         tc_fence_after();
         asm volatile("bar.sync 1, %0;" ::"n"(kGramWork * 32) : "memory");
-        const int pitch = c.Rq + 4, sub = (w >> 2) & 1, q = warp & 3;  // two warps for 32 rows, 16 columns each in turn
-        float* red = reinterpret_cast<float*>(smem) + (size_t)(sub * 128 + 32 * q + lane) * pitch;
-        for (int col = 16 * (w >> 3); col < c.Rq; col += 32) {
+        // the sums, [128][256] at a pitch of 257: lanes store rows and read columns without conflicts
+        const int q = warp & 3, row = 32 * q + lane;
+        float* red = reinterpret_cast<float*>(smem) + row * kGramPitch;
+        const bool used = (stacked ? row & 63 : row) < c.R;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int col = 64 * (w >> 2) + 16 * e;
             uint32_t r[16];
             if (sums) {
-                tmem_ld16(tmem + (uint32_t)(sub * c.Rq + col) + ((uint32_t)(32 * q) << 16), r);
+                tmem_ld16(tmem + (uint32_t)col + ((uint32_t)(32 * q) << 16), r);
             } else {
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    r[e] = 0u;
+                for (int j = 0; j < 16; ++j)
+                    r[j] = 0u;
             }
+            if (used)
 #pragma unroll
-            for (int e = 0; e < 16; e += 4)
-                *reinterpret_cast<uint4*>(red + col + e) = make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
+                for (int j = 0; j < 16; ++j)
+                    red[col + j] = __uint_as_float(r[j]);
         }
         tc_fence_before();
     }
@@ -1208,8 +1219,7 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
     cluster_sync();
     if (warp > kLoadWarps) {
         // CTA j adds the cluster's parts of its share of the 256 columns, in order
-        const int share = 256 / z, row0 = rank * share, pitch = c.Rq + 4;
-        const uint32_t mine = smem_u32(smem);
+        const int share = 256 / z, row0 = rank * share;
         float to, back = 1.f;
         if constexpr (f16)
             half_scale<T>(adapter_max(c, i, of_dy ? 1 : 0, p.parts, lane), to, back);
@@ -1222,28 +1232,34 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
         int row = of_dy ? (tid - (kLoadWarps + 1) * 32) / per : (tid - (kLoadWarps + 1) * 32) % share;
         int r4 = of_dy ? (tid - (kLoadWarps + 1) * 32) % per : (tid - (kLoadWarps + 1) * 32) / share;
         const int step_row = of_dy ? kGramWork * 32 / per : 0, step_r4 = of_dy ? kGramWork * 32 % per : kGramWork * 32 / share;
-#pragma unroll 4
+#pragma unroll 2
         for (int e = tid - (kLoadWarps + 1) * 32; e < items; e += kGramWork * 32) {
             const int64_t n = n0 + row0 + row;
             float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
             if (n < ncols && tokens > 0) {
-                const uint32_t from = mine + (uint32_t)((row0 + row) * pitch + 4 * r4) * 4u;
+                const float* red = reinterpret_cast<const float*>(smem) + 4 * r4 * kGramPitch + row0 + row;
+                float t[4] = {0.f, 0.f, 0.f, 0.f};
                 if (z == 1) {
-                    s = *reinterpret_cast<const float4*>(smem + (from - mine));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        t[j] = red[j * kGramPitch] + (stacked ? red[(64 + j) * kGramPitch] : 0.f);
                 } else {
-                    float4 part[8];
+                    const uint32_t from = smem_u32(red);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        part[k] = k < z ? ld_peer_v4(peer_smem(from, (uint32_t)k)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int j = 0; j < 4; ++j) {
+                        float part[kMaxGramSplit], more[kMaxGramSplit];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        s.x += part[k].x;
-                        s.y += part[k].y;
-                        s.z += part[k].z;
-                        s.w += part[k].w;
+                        for (int k = 0; k < kMaxGramSplit; ++k) {
+                            const uint32_t at = peer_smem(from + j * kGramPitch * 4u, (uint32_t)(k < z ? k : 0));
+                            part[k] = k < z ? ld_peer(at) : 0.f;
+                            more[k] = k < z && stacked ? ld_peer(at + 64 * kGramPitch * 4u) : 0.f;
+                        }
+#pragma unroll
+                        for (int k = 0; k < kMaxGramSplit; ++k)
+                            t[j] += part[k] + more[k];
                     }
                 }
-                s = make_float4(s.x * sc, s.y * sc, s.z * sc, s.w * sc);
+                s = make_float4(t[0] * sc, t[1] * sc, t[2] * sc, t[3] * sc);
             }
             if (n < ncols) {
                 if (of_dy) {
@@ -1456,7 +1472,7 @@ cudaError_t launch_grams(const Common& c, const AdapterBwdArgs& a, cudaStream_t 
     p.da = a.da;
     p.db = a.db;
     p.parts = narrow_split(c, a.N);
-    p.tmem_cols = (int)tmem_columns(2 * c.Rq);
+    p.tmem_cols = 256;
     if (!row_maps(p.dy, tm_type<T>(), 2, a.dy, c.M, a.N) ||
         !(a.q ? row_maps(p.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.q, c.M, a.K)
               : row_maps(p.x, tm_type<T>(), 2, a.x, c.M, a.K)) ||
@@ -1466,7 +1482,7 @@ cudaError_t launch_grams(const Common& c, const AdapterBwdArgs& a, cudaStream_t 
     const int64_t jobs = (int64_t)c.L * (p.strips_y + p.strips_x);
     // split an adapter's tokens until every SM has work, at least two steps each on average
     int z = 1;
-    while (z < 8 && jobs * z < dev.sm_count && c.M / c.L / 64 >= 4 * z)
+    while (z < kMaxGramSplit && jobs * z < dev.sm_count && c.M / c.L / 64 >= 4 * z)
         z *= 2;
     return launch(adapters_gram_kernel<T>, dim3((unsigned)z, (unsigned)jobs), kGramThreads, p.room + 1024, z, p, st);
 }
