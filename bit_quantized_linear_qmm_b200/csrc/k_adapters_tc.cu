@@ -961,7 +961,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32) adapters_decode_kernel(cons
 //   warps 5..20  codes: s q in fp32, rounded once to the operand type, into a ring of two buffers;
 //                rows past the adapter's last token: zeros (only there, so what another adapter's
 //                row holds enters no sum); then the epilogue
-constexpr int kGramWork = 16;  // 8 took 1950 cycles to decode a step, twice what its loads take
+constexpr int kGramWork = 16;
 constexpr int kGramThreads = (kLoadWarps + 1 + kGramWork) * 32;
 constexpr int kGramMaxStages = 6;
 constexpr int kGramPitch = 257;
@@ -1000,7 +1000,7 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&ready[b], kGramWork);
+            mbar_init(&ready[b], kGramWork / 2);
             mbar_init(&taken[b], 1);
         }
         mbar_init(&acc_full, 1);
@@ -1102,37 +1102,38 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
         const int w = warp - kLoadWarps - 1;
         bool ok = true;
         if (of_q) {
-            // 64-column atom w & 3, rows 16 (w >> 2) .. +15: two chunks of 16 codes a thread; the
-            // rows of a phase (r and r + 4) meet no bank twice, loading or storing
-            const int atom = w & 3, row0 = (w >> 2) * 16 + (lane >> 3) + ((lane >> 2) & 1) * 4;
+            // warps 0 - 7 take the even steps, 8 - 15 the odd ones; 64-column atom w & 3, rows 32 (w & 4) / 4
+            // .. +31: four chunks of 16 codes a thread; the rows of a phase (r and r + 4) meet no bank
+            // twice, loading or storing
+            const int odd = w >> 3, atom = w & 3, row0 = (w >> 2 & 1) * 32 + (lane >> 3) + ((lane >> 2) & 1) * 4;
             const int unit = (atom & 1) * 4 + (lane & 3), bunit = 2 * (lane & 3), swap = (lane >> 2) & 1;
             const int64_t k = n0 + atom * 64;
             const float* sc = k < p.K ? p.q_scale + (k >> p.g_shift) * c.M : nullptr;
-            // a step's tokens are read two steps ahead, their scales one
-            float next[2];
-            int tok[2];
+            // a step's tokens are read two of this warp's steps ahead, their scales one
+            float next[4];
+            int tok[4];
             auto load_tokens = [&](int it) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
+                for (int e = 0; e < 4; ++e) {
                     const int row = row0 + 8 * e;
                     tok[e] = it < n_st && sc && row < rows_of(it) ? c.plan.perm[seg0 + (rank + it * z) * 64 + row] : -1;
                 }
             };
             auto load_scales = [&]() {
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
+                for (int e = 0; e < 4; ++e)
                     next[e] = tok[e] >= 0 ? __ldg(sc + tok[e]) : 0.f;
             };
-            load_tokens(0);
+            load_tokens(odd);
             load_scales();
-            load_tokens(1);
-            for (int it = 0; it < n_st; ++it) {
-                float s[2];
+            load_tokens(odd + 2);
+            for (int it = odd; it < n_st; it += 2) {
+                float s[4];
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
+                for (int e = 0; e < 4; ++e)
                     s[e] = next[e];
                 load_scales();
-                load_tokens(it + 2);
+                load_tokens(it + 4);
                 const int slot = it % stages, b = it & 1;
                 if (!mbar_wait_bounded(&full[slot], (it / stages) & 1, c.status) ||
                     (it >= 2 && !mbar_wait_bounded(&taken[b], ((it >> 1) & 1) ^ 1, c.status)) || aborted(&abort_flag)) {
@@ -1141,12 +1142,12 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
                 }
                 const uint8_t* raw = S(slot) + (atom >> 1) * kAtom;
                 const uint32_t dst = smem_u32(D(b)) + atom * kAtom;
-                uint4 v[2];
+                uint4 v[4];
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
+                for (int e = 0; e < 4; ++e)
                     v[e] = *reinterpret_cast<const uint4*>(raw + swz128(row0 + 8 * e, unit));
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
+                for (int e = 0; e < 4; ++e) {
                     const uint32_t cw[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
                     uint32_t o[8];
 #pragma unroll
@@ -1180,12 +1181,12 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
             ok = mbar_wait_bounded(&full[slot], (it / stages) & 1, c.status);
             if (ok) {
                 const uint32_t s0 = smem_u32(S(slot));
-                for (int e = w * 32 + lane; e < (64 - r0) * 32; e += kGramWork * 32)
+                for (int e = w * 32 + lane; e < (64 - r0) * 32 && w < kGramWork / 2; e += kGramWork * 16)
                     st_shared_v4(s0 + ((e & 31) >> 3) * kAtom + (r0 + (e >> 5)) * 128 + (e & 7) * 16, 0u, 0u, 0u, 0u);
                 fence_proxy_async_smem();
             }
             __syncwarp();
-            if (ok && lane == 0)
+            if (ok && lane == 0 && w < kGramWork / 2)
                 mbar_arrive(&ready[0]);
         }
         if (!ok)

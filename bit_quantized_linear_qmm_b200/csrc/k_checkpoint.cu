@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(256) dequantize_int8_groups_kernel(const int8_
 //                 boxes {128 bytes, 64 tokens}
 //   warp 1        512 columns of tensor memory; one thread (of the pair: in CTA 0) issues the MMAs,
 //                 two of them (the pair) on each decoded K = 16 step
-//   warps 2..     decode: 16 codes (one 16-byte load) -> s q in fp32, rounded once to the operand
+//   warps 2..17   decode (of the pair: two groups that take stages in turn): 16 codes (one 16-byte load) -> s q in fp32, rounded once to the operand
 //                 type, two 16-byte swizzled stores.  Eight lanes of a load or store phase cover
 //                 rows r and r + 4 of one 64-input atom, which meet no bank twice.  In the first
 //                 column of tiles they also add up dy's columns: db
@@ -90,7 +90,9 @@ struct WgCfg {
     static constexpr int CN = 128 * SUBS;         // outputs of a CTA
     static constexpr int TN = CN * CTAS;          // outputs of a tile
     static constexpr int CK = kKT / CTAS;         // inputs that a CTA decodes
-    static constexpr int XW = PAIR ? 8 : 16;      // decoding warps: two chunks a thread
+    static constexpr int GROUPS = PAIR ? 2 : 1;   // of decoding warps, taking stages in turn
+    static constexpr int XW = 16;                 // decoding warps
+    static constexpr int GW = XW / GROUPS;        // of a group: two chunks a thread
     static constexpr int EW = 4 * SUBS;
     static constexpr int A_BYTES = CN * kStageM * 2;
     static constexpr int RAW_BYTES = CK * kStageM;
@@ -101,9 +103,10 @@ struct WgCfg {
     static constexpr int STAGE_OUT = EW * 32 * 64;  // staging of the epilogue's warps
     static constexpr int THREADS = (2 + XW + EW) * 32;
     struct Bars {
-        uint64_t full[NS], empty[NS], bfull[NB], bempty[NB], acc_full[2], acc_empty[2], mma_done;
+        uint64_t full[NS], empty[NS], bfull[NB], bempty[NB], acc_full[2], acc_empty[2], mma_done, sums;
         uint32_t tmem;
         int abort_flag;
+        float colsum[CN];       // the odd stages' column sums of dy
     };
     static constexpr int SMEM = NS * SLOT + NB * B_BYTES + STAGE_OUT + (int)sizeof(Bars) + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -253,7 +256,7 @@ __global__ void __launch_bounds__(WgCfg<PAIR>::THREADS, 1) wgrad_tc_kernel(const
             mbar_init(&bars.empty[s], 1);
         }
         for (int b = 0; b < C::NB; ++b) {
-            mbar_init(&bars.bfull[b], C::XW * C::CTAS);
+            mbar_init(&bars.bfull[b], C::GW * C::CTAS);
             mbar_init(&bars.bempty[b], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -261,6 +264,7 @@ __global__ void __launch_bounds__(WgCfg<PAIR>::THREADS, 1) wgrad_tc_kernel(const
             mbar_init(&bars.acc_empty[b], C::EW * C::CTAS);
         }
         mbar_init(&bars.mma_done, 1);
+        mbar_init(&bars.sums, C::GW);
         bars.abort_flag = 0;
         fence_mbar_init();
     }
@@ -351,13 +355,13 @@ __global__ void __launch_bounds__(WgCfg<PAIR>::THREADS, 1) wgrad_tc_kernel(const
         }
         __syncwarp();
     } else if (warp < 2 + C::XW) {
-        constexpr int ATOMS = C::CK / 64, RW = C::XW / ATOMS, RPW = kStageM / RW;  // rows a warp: 16
+        constexpr int ATOMS = C::CK / 64, RW = C::GW / ATOMS, RPW = kStageM / RW;  // rows a warp: 16
         static_assert(RPW == 16, "two chunks a thread");
-        const int w = warp - 2, atom = w % ATOMS;
+        const int group = (warp - 2) / C::GW, w = (warp - 2) % C::GW, atom = w % ATOMS;
         const int row0 = (w / ATOMS) * RPW + (lane >> 3) + ((lane >> 2) & 1) * 4;  // + 8 j, j = 0, 1
         const int unit = (atom & 1) * 4 + (lane & 3), bunit = 2 * (lane & 3), swap = (lane >> 2) & 1;
-        const int ct = (int)threadIdx.x - 64;  // column sums: a column a thread
-        int it = 0;
+        const int ct = w * 32 + lane;  // column sums: a column a thread
+        int it0 = 0, n_sums = 0;       // stages before this tile
         bool ok = true;
         for (int ti = 0; ti < my_tiles && ok; ++ti) {
             const WgUnit wu = wg_unit<PAIR>(unit0 + ti * units, p);
@@ -375,13 +379,15 @@ __global__ void __launch_bounds__(WgCfg<PAIR>::THREADS, 1) wgrad_tc_kernel(const
                     d[j] = sc && m < p.M ? __ldg(sc + m) : 0.f;
                 }
             };
-            load_scales(0, next);
-            for (int mb = 0; mb < nm; ++mb, ++it) {
+            const int mine = C::GROUPS == 2 ? (it0 ^ group) & 1 : 0;  // this group's first stage of the tile
+            load_scales(mine, next);
+            for (int mb = mine; mb < nm; mb += C::GROUPS) {
+                const int it = it0 + mb;
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
                     s[j] = next[j];
-                if (mb + 1 < nm)
-                    load_scales(mb + 1, next);
+                if (mb + C::GROUPS < nm)
+                    load_scales(mb + C::GROUPS, next);
                 const int slot = it % C::NS, b = it % C::NB;
                 if (!mbar_wait_bounded(&bars.full[slot], (it / C::NS) & 1, p.status) ||
                     !mbar_wait_bounded(&bars.bempty[b], ((it / C::NB) & 1) ^ 1, p.status) ||
@@ -433,10 +439,26 @@ __global__ void __launch_bounds__(WgCfg<PAIR>::THREADS, 1) wgrad_tc_kernel(const
                         mbar_arrive(&bars.bfull[b]);
                 }
             }
-            if (sums && here && ok) {
-                const int64_t n = (int64_t)wu.nt * C::TN + rank * C::CN + ct;
-                if (n < p.N)
-                    static_cast<unsigned short*>(p.db)[n] = to_h16(sum, F16);
+            it0 += nm;
+            if (sums && ok) {
+                // the second group hands its sums to the first, which has stages of the next tile to
+                // decode before the second can be here again
+                if (C::GROUPS == 2 && group == 1) {
+                    if (ct < C::CN)
+                        bars.colsum[ct] = sum;
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&bars.sums);
+                } else {
+                    if (C::GROUPS == 2) {
+                        ok = mbar_wait_bounded(&bars.sums, n_sums & 1, p.status);
+                        ++n_sums;
+                        sum += ct < C::CN ? bars.colsum[ct] : 0.f;
+                    }
+                    const int64_t n = (int64_t)wu.nt * C::TN + rank * C::CN + ct;
+                    if (here && ok && n < p.N)
+                        static_cast<unsigned short*>(p.db)[n] = to_h16(sum, F16);
+                }
             }
         }
         if (!ok)
