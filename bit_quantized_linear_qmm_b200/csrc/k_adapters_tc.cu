@@ -1038,11 +1038,23 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
     if (warp < kLoadWarps) {
         const RowMaps& m = of_dy ? p.dy : p.x;
         const int width = of_q ? 128 : 64, blocks = src_bytes / (int)kAtom;  // 128-byte columns: a warp each
+        // a step's tile and tokens are read a step ahead: their latency is longer than a step
+        AdapterTile next;
+        int4 next_tok;
+        auto look = [&](int it) {
+            const int step = rank + it * z;
+            next = c.plan.tiles_l[tile0 + (step >> 1)];
+            next_tok = row_tokens(c.plan, seg0 + step * 64, rows_of(it), lane & 15);
+        };
+        if (n_st > 0)
+            look(0);
         int it = 0;
         for (; it < n_st; ++it) {
             const int slot = it % stages, step = rank + it * z;
-            const AdapterTile d = c.plan.tiles_l[tile0 + (step >> 1)];
-            const int4 tok = row_tokens(c.plan, seg0 + step * 64, rows_of(it), lane & 15);
+            const AdapterTile d = next;
+            const int4 tok = next_tok;
+            if (it + 1 < n_st)
+                look(it + 1);
             const bool ok = it < stages || mbar_wait_bounded(&empty[slot], ((it / stages) & 1) ^ 1, c.status);
             if (__any_sync(0xffffffffu, !ok || aborted(&abort_flag))) {
                 abort_flag = 1;
