@@ -10,8 +10,9 @@
 // tensor cores and the threads only have to keep up.  Tokens are taken in tiles of 128 of one
 // adapter (the plan's list).  A tile whose tokens are consecutive is read in tensor-map boxes of 64
 // rows, any other by tile::gather4, four rows an instruction: no thread touches the data before
-// the tensor cores.  A warp issues one gather in about 86 cycles (its lanes take turns), so four
-// warps share a stage's gathers: one warp alone loaded a gathered tile at half the speed of boxes.
+// the tensor cores.  A thread issues a box in about 150 cycles and a warp a gather in about 86 (its
+// lanes take turns), so four warps share a stage's copies (one thread took 940 cycles for the six of
+// a gram step, longer than anything else in it).
 //
 // h, u and v enter their second product as two 16-bit halves, hi = round(h) and lo = round(h - hi):
 // 2^-16 of the value at most, and two MMAs instead of one.  They are kept in slots, [tile][128][Rq]
@@ -128,15 +129,14 @@ struct RowMaps {
     CUtensorMap box, row;
 };
 
-// One thread: 64 n64 rows from row `first`, 128 bytes of each from column c0.
-QLIN_DEV void load_box(uint32_t dst, const RowMaps& m, int c0, int first, int n64, uint64_t* bar)
+// One thread: a box of 64 rows from row `first`, 128 bytes of each from column c0.
+QLIN_DEV void load_box(uint32_t dst, const CUtensorMap* m, int c0, int first, uint64_t* bar)
 {
-    for (int h = 0; h < n64; ++h)
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-            "[%4];" ::"r"(dst + h * kAtom),
-            "l"(reinterpret_cast<uint64_t>(&m.box)), "r"(c0), "r"(first + 64 * h), "r"(smem_u32(bar))
-            : "memory");
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(first), "r"(smem_u32(bar))
+        : "memory");
 }
 
 // Tokens of rows 4 i .. 4 i + 3 of positions [start, start + count); past the end the first one (its
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kNarrowThreads) adapters_narrow_kernel(const _
         const bool box = d.first >= 0;
         const int4 tok = box || lane >= 8 ? make_int4(0, 0, 0, 0) : row_tokens(c.plan, d.start, d.count, piece);
         int it = 0;
-        for (; it < n_st && (!box || warp == 0); ++it) {
+        for (; it < n_st; ++it) {
             const int slot = it % p.stages;
             const bool ok = it < p.stages || mbar_wait_bounded(&empty[slot], ((it / p.stages) & 1) ^ 1, c.status);
             if (__any_sync(0xffffffffu, !ok || aborted(&abort_flag))) {
@@ -244,16 +244,16 @@ __global__ void __launch_bounds__(kNarrowThreads) adapters_narrow_kernel(const _
                 break;
             }
             const int k = (k_first + it) * 64;
-            if (tid == 0) {
-                mbar_arrive_expect_tx(&full[slot], (unsigned)stage_bytes);
-                if constexpr (FWD) {
-                    tma_load_3d(F(slot), &p.tm_f, k, 0, d.adapter, &full[slot]);
-                } else {
-                    for (int a = 0; a * 64 < c.Rq; ++a)
-                        tma_load_3d(F(slot) + a * kAtom, &p.tm_f, a * 64, k, d.adapter, &full[slot]);
+            if (lane == 0) {
+                if (warp == 0) {
+                    mbar_arrive_expect_tx(&full[slot], (unsigned)stage_bytes);
+                    tma_load_3d(F(slot), &p.tm_f, FWD ? k : 0, FWD ? 0 : k, d.adapter, &full[slot]);
+                } else if (warp == 3) {
+                    if (!FWD && c.Rq > 64)
+                        tma_load_3d(F(slot) + kAtom, &p.tm_f, 64, k, d.adapter, &full[slot]);
+                } else if (box) {
+                    load_box(smem_u32(X(slot)) + (warp - 1) * kAtom, &p.w.box, k, d.first + 64 * (warp - 1), &full[slot]);
                 }
-                if (box)
-                    load_box(smem_u32(X(slot)), p.w, k, d.first, 2, &full[slot]);
             }
             __syncwarp();
             if (!box && lane < 8)
@@ -571,18 +571,17 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapters_wide_kernel(const __
                 if (!ok)
                     break;
                 const int n = b * kWideCols;
-                if (tid == 0) {
-                    mbar_arrive_expect_tx(&full[slot], (unsigned)((none ? 0 : p.f_bytes) + (p.base_p ? base_bytes : 0)));
-                    if (box && p.base_p)
-                        for (int a = 0; a < 2; ++a)
-                            load_box(smem_u32(B(slot)) + a * 2 * kAtom, p.base, n + a * 64, d.first, 2, &full[slot]);
-                    if (none) {
-                    } else if constexpr (FWD) {
-                        for (int a = 0; a < atoms; ++a)
-                            tma_load_3d(F(slot) + a * 2 * kAtom, &p.tm_f, a * 64, n, d.adapter, &full[slot]);
-                    } else {
-                        for (int a = 0; a < 2; ++a)
-                            tma_load_3d(F(slot) + a * c.Rq * 128, &p.tm_f, n + a * 64, 0, d.adapter, &full[slot]);
+                if (lane == 0) {
+                    if (warp == 0)
+                        mbar_arrive_expect_tx(&full[slot], (unsigned)((none ? 0 : p.f_bytes) + (p.base_p ? base_bytes : 0)));
+                    if (box && p.base_p)  // a quarter of base: 64 columns by 64 rows
+                        load_box(smem_u32(B(slot)) + warp * kAtom, &p.base.box, n + (warp >> 1) * 64, d.first + (warp & 1) * 64,
+                                 &full[slot]);
+                    if (!none && warp < (FWD ? atoms : 2)) {
+                        if constexpr (FWD)
+                            tma_load_3d(F(slot) + warp * 2 * kAtom, &p.tm_f, warp * 64, n, d.adapter, &full[slot]);
+                        else
+                            tma_load_3d(F(slot) + warp * c.Rq * 128, &p.tm_f, n + warp * 64, 0, d.adapter, &full[slot]);
                     }
                 }
                 __syncwarp();
@@ -1061,16 +1060,16 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
                 break;
             }
             const uint32_t s0 = smem_u32(S(slot));
-            if (tid == 0) {
-                mbar_arrive_expect_tx(&full[slot], (unsigned)stage_bytes);
-                const int slot0 = (tile0 + (step >> 1)) * kTileL + (step & 1) * 64;
-                for (int half = 0; half < 2; ++half)
-                    for (int a = 0; a * 64 < c.Rq; ++a)
-                        tma_load_2d(H(slot) + half * h_half + a * kAtom, of_dy ? &p.tm_u : &p.tm_v, a * 64,
-                                    (int)(half * c.slots) + slot0, &full[slot]);
-                if (d.first >= 0)
-                    for (int a = 0; a < blocks; ++a)
-                        load_box(s0 + a * kAtom, m, (int)n0 + a * width, d.first + (step & 1) * 64, 1, &full[slot]);
+            if (lane == 0) {
+                if (warp == 0)
+                    mbar_arrive_expect_tx(&full[slot], (unsigned)stage_bytes);
+                if (d.first >= 0 && warp < blocks)
+                    load_box(s0 + warp * kAtom, &m.box, (int)n0 + warp * width, d.first + (step & 1) * 64, &full[slot]);
+                // the atoms of hi, then of lo, from the last warp on
+                const int a = kLoadWarps - 1 - warp, atoms = h_half / (int)kAtom, slot0 = (tile0 + (step >> 1)) * kTileL + (step & 1) * 64;
+                if (a < 2 * atoms)
+                    tma_load_2d(H(slot) + a * kAtom, of_dy ? &p.tm_u : &p.tm_v, a % atoms * 64,
+                                (int)(a / atoms * c.slots) + slot0, &full[slot]);
             }
             __syncwarp();
             if (d.first < 0 && warp < blocks && lane < 16)
