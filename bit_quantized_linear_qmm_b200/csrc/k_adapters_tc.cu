@@ -22,7 +22,8 @@
 //
 // Every mbarrier wait is bounded: on expiry the kernel records the timeout, every role stops, MMAs
 // and copies in flight are waited for and TMEM is freed.
-#include <cstdlib>
+#include <algorithm>
+#include <cmath>
 #include <initializer_list>
 
 #include "adapters.cuh"
@@ -993,6 +994,26 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
     const Common& c = p.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int z = gridDim.x, rank = blockIdx.x;
+    pdl_wait_prior_grids();
+    const int strips = p.strips_y + p.strips_x;
+    const int i = blockIdx.y / strips, strip = blockIdx.y % strips;
+    const bool of_dy = strip < p.strips_y, of_q = !of_dy && p.q_scale;
+    const int64_t n0 = (int64_t)(of_dy ? strip : strip - p.strips_y) * 256, ncols = of_dy ? p.N : p.K;
+    const int seg0 = c.plan.seg[i], tokens = c.plan.seg[i + 1] - seg0, tile0 = c.plan.tile_l0[i];
+    if (tokens == 0) {  // the whole cluster: zeros
+        const int64_t n = ncols - n0 < 256 ? ncols - n0 : 256;
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        if (of_dy) {
+            uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(p.db) + ((size_t)i * p.N + n0) * c.R);
+            for (int64_t e = rank * kGramThreads + tid; e < n * c.R / 8; e += z * kGramThreads)
+                o[e] = zero;
+        } else {
+            const int vecs = (int)(n / 8);
+            for (int e = rank * kGramThreads + tid; e < vecs * c.R; e += z * kGramThreads)
+                *reinterpret_cast<uint4*>(static_cast<T*>(p.da) + ((size_t)i * c.R + e / vecs) * p.K + n0 + 8 * (e % vecs)) = zero;
+        }
+        return;
+    }
     if (tid == 0) {
         for (int s = 0; s < kGramMaxStages; ++s) {
             mbar_init(&full[s], 1);
@@ -1012,14 +1033,7 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_s;
-    pdl_launch_dependents();
-    pdl_wait_prior_grids();
-
-    const int strips = p.strips_y + p.strips_x;
-    const int i = blockIdx.y / strips, strip = blockIdx.y % strips;
-    const bool of_dy = strip < p.strips_y, of_q = !of_dy && p.q_scale;
-    const int64_t n0 = (int64_t)(of_dy ? strip : strip - p.strips_y) * 256, ncols = of_dy ? p.N : p.K;
-    const int seg0 = c.plan.seg[i], tokens = c.plan.seg[i + 1] - seg0, tile0 = c.plan.tile_l0[i];
+    pdl_launch_dependents();  // after the allocation, as in the narrow kernel
     const int steps = (tokens + 63) / 64;
     const int n_st = steps > rank ? (steps - 1 - rank) / z + 1 : 0;  // steps rank, rank + z, ...
     const bool stacked = c.Rq <= 64;  // hi and lo are the two 64-rank atoms of one operand
@@ -1499,6 +1513,23 @@ cudaError_t launch_grams(const Common& c, const AdapterBwdArgs& a, cudaStream_t 
     return launch(adapters_gram_kernel<T>, dim3((unsigned)z, (unsigned)jobs), kGramThreads, p.room + 1024, z, p, st);
 }
 
+// Whether the one-launch kernel is faster than the two tensor-memory ones, by what both cost in us.
+// The host does not know how the tokens fall on the adapters: it takes them as drawn evenly, so
+// `used` adapters have tokens, and an adapter's last tile is half full on average.  Measured on both
+// sides at K, N = 4096 and 11008, ranks 16 - 128, 1 - 1024 tokens, 1 - 100 adapters; e.g. at 4096 x
+// 4096, one launch against two: 1 token rank 16 4.2 / 10.2, rank 128 15.8 / 11.9; 61 tokens of 32
+// adapters rank 64 14.5 / 24.8; 256 of 4 rank 16 6.2 / 12.1, rank 64 21 / 13.4; 1024 of 4 rank 16 23 / 17.
+bool few_tokens(const AdapterFwdArgs& a)
+{
+    const double M = (double)a.M, n = (double)a.L + 1, used = n * (1 - std::exp(-M / n));
+    auto tiles = [&](int t) { return std::max(used, M / t + used / 2); };
+    const double row = (double)(a.K + a.N), longer = (double)std::max(a.K, a.N);
+    // 18 clusters of 8 at a time, each reading its adapter once
+    const double one = 3 + std::ceil(tiles(kTileS) / 18) * 1.4e-5 * rank_up(a.R) * row;
+    const double two = 8 + 4e-4 * longer + tiles(kTileL) * row * 5e-5;
+    return one < two;
+}
+
 template <typename T>
 cudaError_t launch_decode(const Common& c, const AdapterFwdArgs& a, cudaStream_t st)
 {
@@ -1531,7 +1562,7 @@ template <typename T>
 cudaError_t forward_t(const AdapterFwdArgs& a, cudaStream_t st, const DeviceInfo& dev)
 {
     const Common c = common_of(a.plan, a.dt, a.M, a.L, a.R, a.ws, dev);
-    if (getenv("QDEC") ? a.M <= atoi(getenv("QDEC")) : a.M <= 128)
+    if (few_tokens(a))
         return launch_decode<T>(c, a, st);
     const cudaError_t e = launch_narrow<T, true>(c, a.x, a.K, a.a, nullptr, nullptr, a.u, st, dev);
     return e != cudaSuccess ? e : launch_wide<T, true>(c, a.b, a.scales, a.base, a.out, a.N, st, dev);
