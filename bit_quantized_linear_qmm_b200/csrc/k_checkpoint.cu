@@ -20,35 +20,46 @@ namespace {
 
 QLIN_DEV float code_of(uint32_t w, int i) { return (float)(int8_t)(w >> (8 * i)); }
 
-// 16 codes a thread: one 16-byte load, one scale (a group is 64 codes at least), 16-byte stores.
-// Memory-bound: 1 byte in and 2 or 4 out for each value.
+// Restoring: 1 byte in and 2 or 4 out for each value, bound by memory.  A block takes 8 rows by 512
+// columns (a warp a row), whose scales are neighbours in memory; a thread 8 codes at a time, so that
+// its 16-byte stores (two for fp32) follow one another through the warp.
 template <typename T>
 __global__ void __launch_bounds__(256) dequantize_int8_groups_kernel(const int8_t* __restrict__ q,
                                                                      const float* __restrict__ scale, int64_t N,
                                                                      int64_t K, int g_shift, T* __restrict__ out)
 {
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 16;
-    if (i >= N * K)
-        return;
-    const int64_t n = i / K, grp = (i - n * K) >> g_shift;
-    const uint4 v = ldg_stream_v4(q + i);
-    const float s = __ldg(scale + grp * N + n);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    if constexpr (sizeof(T) == 4) {
+    const int lane = threadIdx.x & 31;
+    const int64_t col = (int64_t)blockIdx.x * 512 + 8 * lane;
+    for (int64_t n = (int64_t)blockIdx.y * 8 + (threadIdx.x >> 5); n < N; n += (int64_t)gridDim.y * 8) {
+        uint2 v[2];
+        float s[2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<float4*>(out + i + 4 * j) =
-                make_float4(code_of(w[j], 0) * s, code_of(w[j], 1) * s, code_of(w[j], 2) * s, code_of(w[j], 3) * s);
-    } else {
-        constexpr int f16 = sizeof(T) == 2 && !__is_same(T, __nv_bfloat16);
-        uint32_t h[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            h[2 * j] = pack_h16x2(code_of(w[j], 0) * s, code_of(w[j], 1) * s, f16);
-            h[2 * j + 1] = pack_h16x2(code_of(w[j], 2) * s, code_of(w[j], 3) * s, f16);
+        for (int h = 0; h < 2; ++h) {
+            const int64_t c = col + 256 * h;
+            if (c < K) {
+                v[h] = __ldg(reinterpret_cast<const uint2*>(q + n * K + c));
+                s[h] = __ldg(scale + (c >> g_shift) * N + n);
+            }
         }
-        *reinterpret_cast<uint4*>(out + i) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(out + i + 8) = make_uint4(h[4], h[5], h[6], h[7]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t c = col + 256 * h;
+            if (c >= K)
+                continue;
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                f[i] = code_of(i < 4 ? v[h].x : v[h].y, i & 3) * s[h];
+            T* o = out + n * K + c;
+            if constexpr (sizeof(T) == 4) {
+                *reinterpret_cast<float4*>(o) = make_float4(f[0], f[1], f[2], f[3]);
+                *reinterpret_cast<float4*>(o + 4) = make_float4(f[4], f[5], f[6], f[7]);
+            } else {
+                constexpr int f16 = !__is_same(T, __nv_bfloat16);
+                *reinterpret_cast<uint4*>(o) = make_uint4(pack_h16x2(f[0], f[1], f16), pack_h16x2(f[2], f[3], f16),
+                                                          pack_h16x2(f[4], f[5], f16), pack_h16x2(f[6], f[7], f16));
+            }
+        }
     }
 }
 
@@ -564,7 +575,7 @@ cudaError_t launch_wgrad(WgParams& p, cudaStream_t st, const DeviceInfo& dev)
 cudaError_t launch_dequantize_int8_groups(const int8_t* q, const float* scale, int64_t N, int64_t K, int g, void* out,
                                           qlin_dtype o_dt, cudaStream_t st)
 {
-    const unsigned blocks = (unsigned)((N * K / 16 + 255) / 256);
+    const dim3 blocks((unsigned)((K + 511) / 512), (unsigned)((N + 7) / 8 < 65535 ? (N + 7) / 8 : 65535));
     const int sh = log2_of(g);
     if (o_dt == QLIN_F32)
         dequantize_int8_groups_kernel<float><<<blocks, 256, 0, st>>>(q, scale, N, K, sh, static_cast<float*>(out));

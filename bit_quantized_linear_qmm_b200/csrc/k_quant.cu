@@ -794,45 +794,121 @@ __global__ void __launch_bounds__(256) quantize_int8_groups_kernel(const TW* __r
         scale_w[grp * N + n] = sc;
 }
 
+// max |x| of 16 elements held as loaded (bf16 and fp16 in pairs), NaN left out as fmaxf leaves it out
+QLIN_DEV float amax16(const float4 (&u)[4])
+{
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        a = fmaxf(fmaxf(a, fmaxf(fabsf(u[i].x), fabsf(u[i].y))), fmaxf(fabsf(u[i].z), fabsf(u[i].w)));
+    return a;
+}
+template <typename H2>
+QLIN_DEV float amax16(const uint4 (&u)[2])
+{
+    H2 a = __habs2(*reinterpret_cast<const H2*>(&u[0].x));
+    const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+#pragma unroll
+    for (int i = 1; i < 8; ++i)
+        a = __hmax2(a, __habs2(*reinterpret_cast<const H2*>(&w[i])));
+    const float lo = __low2float(a), hi = __high2float(a);
+    return fmaxf(fmaxf(0.f, lo), hi);
+}
+
 // The same with G/16 lanes per group, 16 consecutive values each (16-byte loads, one 16-byte store
-// of the lane's int8 codes); 16-byte aligned w and q.
+// of the lane's int8 codes); 16-byte aligned w and q.  A block takes 8 rows by 1024 columns, a warp a
+// row, in two halves that are loaded together: the 8 scales of a group are neighbours in memory and
+// leave as one 32-byte sector.  A code is the low byte of fma(x, r, 1.5 2^23), which rounds half to
+// even as rint does; where an element lies within 1e-4 of a half-integer (see rint_div; the fused
+// product is nearer to the quotient than the rounded one there) its 16 take the division.
 template <typename TW, int G>
 __global__ void __launch_bounds__(256) quantize_int8_groups_vec_kernel(const TW* __restrict__ w, int64_t N, int64_t K,
                                                                       int8_t* __restrict__ q,
                                                                       float* __restrict__ scale_w)
 {
-    constexpr int LPG = G / 16;
-    const int64_t ng = K / G, groups = N * ng;
-    const int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    const int64_t gi = t / LPG;
-    const int sub = (int)(t % LPG);
-    // lanes past the last group take part in the butterfly on the last group and store nothing
-    const bool ok = gi < groups;
-    const int64_t gq = ok ? gi : groups - 1;
-    float v[16];
-    load16(w + gq * G + 16 * sub, v);
-    float amax = 0.f;
+    constexpr int LPG = G / 16, GPH = 32 / LPG;     // lanes a group, groups of a warp's half
+    constexpr int NV = sizeof(TW) == 4 ? 4 : 2;     // 16-byte loads of 16 elements
+    __shared__ float sc_s[2][2 * GPH][8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int buf = 0;
+    for (int64_t n0 = (int64_t)blockIdx.y * 8; n0 < N; n0 += (int64_t)gridDim.y * 8, buf ^= 1) {
+        const int64_t n = n0 + warp;
+        uint4 raw[2][NV];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        amax = fmaxf(amax, fabsf(v[i]));
+        for (int h = 0; h < 2; ++h) {
+            const int64_t col = (int64_t)blockIdx.x * 1024 + 512 * h + 16 * lane;
 #pragma unroll
-    for (int o = 1; o < LPG; o <<= 1)
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    float sc = __fdiv_rn(amax, 127.0f);
-    if (sc == 0.f)
-        sc = 1.f;
-    const float rsc = __frcp_rn(sc);
-    const bool fast = rcp_ok(sc);
-    int c[16];
+            for (int i = 0; i < NV; ++i)  // a group's lanes are all in or all out
+                raw[h][i] = n < N && col < K ? __ldg(reinterpret_cast<const uint4*>(w + n * K + col) + i)
+                                             : make_uint4(0u, 0u, 0u, 0u);
+        }
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        c[i] = sym_code(v[i], sc, rsc, fast);
-    const uint32_t word[4] = {pack4(c[0], c[1], c[2], c[3]), pack4(c[4], c[5], c[6], c[7]),
-                              pack4(c[8], c[9], c[10], c[11]), pack4(c[12], c[13], c[14], c[15])};
-    if (ok) {
-        *reinterpret_cast<uint4*>(q + gi * G + 16 * sub) = make_uint4(word[0], word[1], word[2], word[3]);
-        if (sub == 0)
-            scale_w[(gi % ng) * N + gi / ng] = sc;
+        for (int h = 0; h < 2; ++h) {
+            const int64_t col = (int64_t)blockIdx.x * 1024 + 512 * h + 16 * lane;
+            float amax;
+            float v[16];
+            const uint32_t* u = reinterpret_cast<const uint32_t*>(raw[h]);
+            if constexpr (sizeof(TW) == 4) {
+                float4 f[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    f[i] = *reinterpret_cast<const float4*>(&raw[h][i]);
+                amax = amax16(f);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    v[i] = __uint_as_float(u[i]);
+            } else {
+                if constexpr (__is_same(TW, __half))
+                    amax = amax16<__half2>(raw[h]);
+                else
+                    amax = amax16<__nv_bfloat162>(raw[h]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    v[2 * i] = lo_half_to_float(u[i], static_cast<const TW*>(nullptr));
+                    v[2 * i + 1] = hi_half_to_float(u[i], static_cast<const TW*>(nullptr));
+                }
+            }
+#pragma unroll
+            for (int o = 1; o < LPG; o <<= 1)
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            float sc = __fdiv_rn(amax, 127.0f);
+            if (sc == 0.f)
+                sc = 1.f;
+            const float rsc = __frcp_rn(sc);
+            const bool fast = rcp_ok(sc);
+            uint32_t word[4];
+            bool near = !fast;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t b[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float x = v[4 * j + e];
+                    const float t = __fmaf_rn(x, rsc, 12582912.f);
+                    const float d = __fmaf_rn(x, rsc, __fsub_rn(12582912.f, t));
+                    near |= !(fabsf(d) < 0.4999f);  // true for NaN
+                    b[e] = __float_as_uint(t);
+                }
+                word[j] = prmt(prmt(b[0], b[1], 0x0040u), prmt(b[2], b[3], 0x0040u), 0x5410u);
+            }
+            if (near) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    word[j] = pack4(sym_code(v[4 * j], sc, rsc, fast), sym_code(v[4 * j + 1], sc, rsc, fast),
+                                    sym_code(v[4 * j + 2], sc, rsc, fast), sym_code(v[4 * j + 3], sc, rsc, fast));
+            }
+            if (n < N && col < K)
+                *reinterpret_cast<uint4*>(q + n * K + col) = make_uint4(word[0], word[1], word[2], word[3]);
+            if (lane % LPG == 0)
+                sc_s[buf][GPH * h + lane / LPG][warp] = sc;
+        }
+        __syncthreads();  // the other buffer is written next, so one barrier a turn is enough
+        if (threadIdx.x < 2 * GPH * 8) {
+            const int g = threadIdx.x >> 3, r = threadIdx.x & 7;
+            const int64_t grp = (int64_t)blockIdx.x * (2 * GPH) + g;
+            if (n0 + r < N && grp < K / G)
+                scale_w[grp * N + n0 + r] = sc_s[buf][g][r];
+        }
     }
 }
 
@@ -1110,7 +1186,7 @@ cudaError_t launch_quantize_int8_groups(const void* w, qlin_dtype w_dt, int64_t 
 {
     const bool vec = ((reinterpret_cast<uintptr_t>(w) | reinterpret_cast<uintptr_t>(q)) & 15u) == 0;
     const unsigned blocks = (unsigned)((N * (K / g) + 7) / 8);
-    const unsigned vblocks = (unsigned)((N * (K / g) * (g / 16) + 255) / 256);
+    const dim3 vblocks((unsigned)((K + 1023) / 1024), (unsigned)((N + 7) / 8 < 65535 ? (N + 7) / 8 : 65535));
 #define QLIN_QG(TW, G)                                                                                               \
     do {                                                                                                             \
         if (vec)                                                                                                     \
