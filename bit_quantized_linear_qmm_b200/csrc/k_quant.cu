@@ -816,98 +816,97 @@ QLIN_DEV float amax16(const uint4 (&u)[2])
 }
 
 // The same with G/16 lanes per group, 16 consecutive values each (16-byte loads, one 16-byte store
-// of the lane's int8 codes); 16-byte aligned w and q.  A block takes 8 rows by 1024 columns, a warp a
-// row, in two halves that are loaded together: the 8 scales of a group are neighbours in memory and
-// leave as one 32-byte sector.  A code is the low byte of fma(x, r, 1.5 2^23), which rounds half to
-// even as rint does; where an element lies within 1e-4 of a half-integer (see rint_div; the fused
-// product is nearer to the quotient than the rounded one there) its 16 take the division.
+// of the lane's int8 codes); 16-byte aligned w and q.  A warp takes 8 rows by 512 columns, four rows
+// (fp32: two) at a time: lane l of a group divides for row l mod 4 and hands scale and reciprocal to
+// the others, and the 8 scales of a group fill one 32-byte sector.  A code is the low byte of
+// fma(x, r, 1.5 2^23), the product rounded half to even as rint does it.  With r = (1/s)(1 + e1) the
+// product and the rounded quotient q (1 + e3) differ by less than 2 2^-24 127 = 1.6e-5, so they round
+// alike unless the product lies within 3e-5 of a half-integer; such an element takes the division.
 template <typename TW, int G>
 __global__ void __launch_bounds__(256) quantize_int8_groups_vec_kernel(const TW* __restrict__ w, int64_t N, int64_t K,
                                                                       int8_t* __restrict__ q,
-                                                                      float* __restrict__ scale_w)
+                                                                      float* __restrict__ scale_w, int rows_of_warp)
 {
-    constexpr int LPG = G / 16, GPH = 32 / LPG;     // lanes a group, groups of a warp's half
+    constexpr int LPG = G / 16;                     // lanes a group
     constexpr int NV = sizeof(TW) == 4 ? 4 : 2;     // 16-byte loads of 16 elements
-    __shared__ float sc_s[2][2 * GPH][8];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int buf = 0;
-    for (int64_t n0 = (int64_t)blockIdx.y * 8; n0 < N; n0 += (int64_t)gridDim.y * 8, buf ^= 1) {
-        const int64_t n = n0 + warp;
-        uint4 raw[2][NV];
+    constexpr int RPT = sizeof(TW) == 4 ? 2 : 4;    // rows at a time
+    const int lane = threadIdx.x & 31, first = lane & ~(LPG - 1), my = lane & (RPT - 1);
+    const int64_t col = (int64_t)blockIdx.x * 512 + 16 * lane;
+    const bool in = col < K;  // a group's lanes are all in or all out
+    const int64_t warps = blockDim.x >> 5, stride = gridDim.y * warps * rows_of_warp;
+    for (int64_t rows = ((int64_t)blockIdx.y * warps + (threadIdx.x >> 5)) * rows_of_warp; rows < N; rows += stride) {
+#pragma unroll 1
+        for (int64_t n = rows; n < rows + rows_of_warp && n < N; n += RPT) {
+            uint4 raw[RPT][NV];
+            float amax[RPT];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t col = (int64_t)blockIdx.x * 1024 + 512 * h + 16 * lane;
+            for (int j = 0; j < RPT; ++j)
 #pragma unroll
-            for (int i = 0; i < NV; ++i)  // a group's lanes are all in or all out
-                raw[h][i] = n < N && col < K ? __ldg(reinterpret_cast<const uint4*>(w + n * K + col) + i)
-                                             : make_uint4(0u, 0u, 0u, 0u);
-        }
+                for (int i = 0; i < NV; ++i)
+                    raw[j][i] = in && n + j < N ? __ldg(reinterpret_cast<const uint4*>(w + (n + j) * K + col) + i)
+                                                : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t col = (int64_t)blockIdx.x * 1024 + 512 * h + 16 * lane;
-            float amax;
-            float v[16];
-            const uint32_t* u = reinterpret_cast<const uint32_t*>(raw[h]);
-            if constexpr (sizeof(TW) == 4) {
-                float4 f[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    f[i] = *reinterpret_cast<const float4*>(&raw[h][i]);
-                amax = amax16(f);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    v[i] = __uint_as_float(u[i]);
-            } else {
-                if constexpr (__is_same(TW, __half))
-                    amax = amax16<__half2>(raw[h]);
+            for (int j = 0; j < RPT; ++j) {
+                if constexpr (sizeof(TW) == 4)
+                    amax[j] = amax16(reinterpret_cast<const float4(&)[4]>(raw[j]));
+                else if constexpr (__is_same(TW, __half))
+                    amax[j] = amax16<__half2>(raw[j]);
                 else
-                    amax = amax16<__nv_bfloat162>(raw[h]);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    v[2 * i] = lo_half_to_float(u[i], static_cast<const TW*>(nullptr));
-                    v[2 * i + 1] = hi_half_to_float(u[i], static_cast<const TW*>(nullptr));
-                }
+                    amax[j] = amax16<__nv_bfloat162>(raw[j]);
             }
 #pragma unroll
             for (int o = 1; o < LPG; o <<= 1)
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            float sc = __fdiv_rn(amax, 127.0f);
+#pragma unroll
+                for (int j = 0; j < RPT; ++j)
+                    amax[j] = fmaxf(amax[j], __shfl_xor_sync(0xffffffffu, amax[j], o));
+            float a = amax[0];
+#pragma unroll
+            for (int j = 1; j < RPT; ++j)
+                a = my == j ? amax[j] : a;
+            float sc = __fdiv_rn(a, 127.0f);
             if (sc == 0.f)
                 sc = 1.f;
-            const float rsc = __frcp_rn(sc);
-            const bool fast = rcp_ok(sc);
-            uint32_t word[4];
-            bool near = !fast;
+            // a scale whose reciprocal is not normal: NaN, so that every element divides
+            const float rsc = rcp_ok(sc) ? __frcp_rn(sc) : __uint_as_float(0x7fc00000u);
+            if (in && (lane & (LPG - 1)) < RPT && n + my < N)
+                scale_w[(col / G) * N + n + my] = sc;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t b[4];
+            for (int j = 0; j < RPT; ++j) {
+                const float s = __shfl_sync(0xffffffffu, sc, first + j), r = __shfl_sync(0xffffffffu, rsc, first + j);
+                const uint32_t* u = reinterpret_cast<const uint32_t*>(raw[j]);
+                auto value = [&](int i) {
+                    if constexpr (sizeof(TW) == 4)
+                        return __uint_as_float(u[i]);
+                    else
+                        return i & 1 ? hi_half_to_float(u[i >> 1], static_cast<const TW*>(nullptr))
+                                     : lo_half_to_float(u[i >> 1], static_cast<const TW*>(nullptr));
+                };
+                auto off = [&](float x, float t) { return !(fabsf(__fmaf_rn(x, r, __fsub_rn(12582912.f, t))) < 0.49997f); };
+                uint32_t word[4];
+                bool near = false;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float x = v[4 * j + e];
-                    const float t = __fmaf_rn(x, rsc, 12582912.f);
-                    const float d = __fmaf_rn(x, rsc, __fsub_rn(12582912.f, t));
-                    near |= !(fabsf(d) < 0.4999f);  // true for NaN
-                    b[e] = __float_as_uint(t);
-                }
-                word[j] = prmt(prmt(b[0], b[1], 0x0040u), prmt(b[2], b[3], 0x0040u), 0x5410u);
-            }
-            if (near) {
+                    uint32_t b[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    word[j] = pack4(sym_code(v[4 * j], sc, rsc, fast), sym_code(v[4 * j + 1], sc, rsc, fast),
-                                    sym_code(v[4 * j + 2], sc, rsc, fast), sym_code(v[4 * j + 3], sc, rsc, fast));
+                    for (int i = 0; i < 4; ++i) {
+                        const float x = value(4 * e + i), t = __fmaf_rn(x, r, 12582912.f);
+                        near |= off(x, t);  // true for NaN
+                        b[i] = __float_as_uint(t);
+                    }
+                    word[e] = prmt(prmt(b[0], b[1], 0x0040u), prmt(b[2], b[3], 0x0040u), 0x5410u);
+                }
+                if (near) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float x = value(i);
+                        if (off(x, __fmaf_rn(x, r, 12582912.f)))
+                            word[i >> 2] = (word[i >> 2] & ~(0xffu << (8 * (i & 3)))) |
+                                           ((uint32_t)sym_code(x, s, r, false) & 0xffu) << (8 * (i & 3));
+                    }
+                }
+                if (in && n + j < N)
+                    *reinterpret_cast<uint4*>(q + (n + j) * K + col) = make_uint4(word[0], word[1], word[2], word[3]);
             }
-            if (n < N && col < K)
-                *reinterpret_cast<uint4*>(q + n * K + col) = make_uint4(word[0], word[1], word[2], word[3]);
-            if (lane % LPG == 0)
-                sc_s[buf][GPH * h + lane / LPG][warp] = sc;
-        }
-        __syncthreads();  // the other buffer is written next, so one barrier a turn is enough
-        if (threadIdx.x < 2 * GPH * 8) {
-            const int g = threadIdx.x >> 3, r = threadIdx.x & 7;
-            const int64_t grp = (int64_t)blockIdx.x * (2 * GPH) + g;
-            if (n0 + r < N && grp < K / G)
-                scale_w[grp * N + n0 + r] = sc_s[buf][g][r];
         }
     }
 }
@@ -1182,16 +1181,22 @@ cudaError_t launch_quantize_weight_int8_clip(const void* w, qlin_dtype w_dt, int
 }
 
 cudaError_t launch_quantize_int8_groups(const void* w, qlin_dtype w_dt, int64_t N, int64_t K, int g, int8_t* q,
-                                        float* scale_w, cudaStream_t st, const DeviceInfo&)
+                                        float* scale_w, cudaStream_t st, const DeviceInfo& dev)
 {
     const bool vec = ((reinterpret_cast<uintptr_t>(w) | reinterpret_cast<uintptr_t>(q)) & 15u) == 0;
     const unsigned blocks = (unsigned)((N * (K / g) + 7) / 8);
-    const dim3 vblocks((unsigned)((K + 1023) / 1024), (unsigned)((N + 7) / 8 < 65535 ? (N + 7) / 8 : 65535));
+    // a block: 8 warps of 8 rows by 512 columns; where that is less than two blocks an SM, one warp of 4
+    // rows (64 x 4096: 8.8 -> 4 us)
+    const int64_t across = (K + 511) / 512;
+    const bool few = across * ((N + 63) / 64) < 2 * dev.sm_count;
+    const int rows = few ? 4 : 8, threads = few ? 32 : 256;
+    const int64_t down = few ? (N + 3) / 4 : (N + 63) / 64;
+    const dim3 vblocks((unsigned)across, (unsigned)(down < 65535 ? down : 65535));
 #define QLIN_QG(TW, G)                                                                                               \
     do {                                                                                                             \
         if (vec)                                                                                                     \
             quantize_int8_groups_vec_kernel<TW, G>                                                                   \
-                <<<vblocks, 256, 0, st>>>(static_cast<const TW*>(w), N, K, q, scale_w);                              \
+                <<<vblocks, threads, 0, st>>>(static_cast<const TW*>(w), N, K, q, scale_w, rows);                    \
         else                                                                                                         \
             quantize_int8_groups_kernel<TW, G><<<blocks, 256, 0, st>>>(static_cast<const TW*>(w), N, K, q, scale_w); \
     } while (0)

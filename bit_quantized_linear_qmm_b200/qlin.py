@@ -118,13 +118,13 @@ def _stream(device=None):
 
 
 def _dt(t: torch.Tensor) -> int:
-    if t.dtype == torch.float32:
-        return QLIN_F32
-    if t.dtype == torch.bfloat16:
-        return QLIN_BF16
-    if t.dtype == torch.float16:
-        return QLIN_F16
-    raise TypeError(f"unsupported dtype {t.dtype}")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
+
+
+_DTYPES = {torch.float32: QLIN_F32, torch.bfloat16: QLIN_BF16, torch.float16: QLIN_F16}
 
 
 def _torch_dt(code: int):
@@ -280,13 +280,16 @@ def device_status(device=None) -> int:
 
 
 def quantize_int8_groups(w, group_size: int):
-    """Per-group symmetric int8 weights: (q int8 [N, K], scale_w fp32 [K/group_size, N])."""
-    _cuda(w)
+    """Per-group symmetric int8 weights: (q int8 [N, K], scale_w fp32 [K/group_size, N]).
+
+    Of a layer's input it is the 8-bit checkpoint that dequantize_int8_groups restores and adapters_backward and
+    pergroup_wgrad take."""
     N, K = w.shape
-    q = torch.empty((N, K), dtype=torch.int8, device=w.device)
-    s = torch.empty((K // group_size, N), dtype=torch.float32, device=w.device)
-    _check(lib().qlin_quantize_int8_groups(_ptr(w), _dt(w), N, K, group_size, _ptr(q), _ptr(s), _stream(w.device)),
-           "qlin_quantize_int8_groups")
+    dev = w.get_device()
+    q = w.new_empty((N, K), dtype=torch.int8)
+    s = w.new_empty((K // group_size, N), dtype=torch.float32)
+    _run("qlin_quantize_int8_groups", dev, _fit("w", w, (N, K), w.dtype, dev), _dt(w), N, K, group_size, q.data_ptr(),
+         s.data_ptr())
     return q, s
 
 
@@ -338,7 +341,7 @@ def _fit(name, t, shape, dtype, dev):
 def _space(workspace, need: int, dev: int, like):
     """(address, bytes) of the caller's workspace, or of one from torch's allocator; the tensor keeps it alive."""
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+        workspace = like.new_empty((need,), dtype=torch.uint8)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on cuda:{dev}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -346,7 +349,7 @@ def _space(workspace, need: int, dev: int, like):
 
 def _run(name, dev: int, *args):
     """Calls a library function on device dev and its current stream."""
-    fn = getattr(lib(), name)
+    fn = getattr(_lib or lib(), name)
     if torch.cuda.current_device() == dev:
         status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
     else:
@@ -402,7 +405,7 @@ def adapters_forward(x, a, b, scales, plan: AdapterPlan, base=None, out=None, u=
     M, N, K, L, R, dev = _adapter_sizes(x, a, b, plan)
     dt = x.dtype
     if out is None:
-        out = torch.empty((M, N), dtype=dt, device=x.device)
+        out = x.new_empty((M, N))
     ws, wp, wn = _space(workspace, lib().qlin_adapters_workspace_size(M, N, K, L, R, 0), dev, x)
     _run("qlin_adapters_forward", dev, _fit("x", x, (M, K), dt, dev), _dt(x), M, K, _fit("a", a, (L, R, K), dt, dev),
          _fit("b", b, (L, N, R), dt, dev), _fit("scales", scales, (L,), torch.float32, dev), L, R, N,
@@ -426,7 +429,7 @@ def adapters_backward(dy, a, b, scales, plan: AdapterPlan, u, x=None, checkpoint
     if not want_dx and (dx is not None or dx_base is not None):
         raise ValueError("dx and dx_base belong to want_dx=True")
     if dx is None and want_dx:
-        dx = torch.empty((M, K), dtype=dt, device=dy.device)
+        dx = dy.new_empty((M, K))
     ap, bp = _fit("a", a, (L, R, K), dt, dev), _fit("b", b, (L, N, R), dt, dev)
     da, db = torch.empty_like(a), torch.empty_like(b)
     ws, wp, wn = _space(workspace, lib().qlin_adapters_workspace_size(M, N, K, L, R, 1), dev, dy)
@@ -445,7 +448,7 @@ def dequantize_int8_groups(q, scale, group_size: int, out_dtype=torch.bfloat16, 
     N, K = q.shape
     dev = q.get_device()
     if out is None:
-        out = torch.empty((N, K), dtype=out_dtype, device=q.device)
+        out = q.new_empty((N, K), dtype=out_dtype)
     _run("qlin_dequantize_int8_groups", dev, _fit("q", q, (N, K), torch.int8, dev),
          _fit("scale", scale, (K // group_size if group_size > 0 else 0, N), torch.float32, dev), N, K, group_size,
          _fit("out", out, (N, K), out_dtype, dev), _dt(out))
@@ -459,8 +462,8 @@ def pergroup_wgrad(dy, q, scale, group_size: int, bias: bool = True, dw=None):
     M, N = dy.shape
     K, dt, dev = q.shape[1], dy.dtype, dy.get_device()
     if dw is None:
-        dw = torch.empty((N, K), dtype=dt, device=dy.device)
-    db = torch.empty((N,), dtype=dt, device=dy.device) if bias else None
+        dw = dy.new_empty((N, K))
+    db = dy.new_empty((N,)) if bias else None
     _run("pergroup_wgrad", dev, _fit("dy", dy, (M, N), dt, dev), _dt(dy), M, N, _fit("q", q, (M, K), torch.int8, dev),
          _fit("scale", scale, (K // group_size if group_size > 0 else 0, M), torch.float32, dev), K, group_size,
          _fit("dw", dw, (N, K), dt, dev), None if db is None else db.data_ptr())
