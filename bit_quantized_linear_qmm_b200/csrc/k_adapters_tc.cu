@@ -988,7 +988,7 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
     constexpr int f16 = Is16<T>::f16;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t full[kGramMaxStages], empty[kGramMaxStages], ready[2], taken[2], acc_full;
+    __shared__ uint64_t full[kGramMaxStages], empty[kGramMaxStages], ready[2], taken[2], acc_full, tail;
     __shared__ uint32_t tmem_s;
     __shared__ int abort_flag;
     const Common& c = p.c;
@@ -1024,6 +1024,7 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
             mbar_init(&taken[b], 1);
         }
         mbar_init(&acc_full, 1);
+        mbar_init(&tail, 1);
         abort_flag = 0;
         fence_mbar_init();
     }
@@ -1101,9 +1102,12 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
             for (int it = 0; it < n_st && ok; ++it) {
                 const int slot = it % stages, b = it & 1;
                 ok = mbar_wait_bounded(&full[slot], (it / stages) & 1, c.status);
-                // worked steps use the two ready barriers in turn (without codes: one step, the last)
-                if (ok && worked(it))
+                if (ok && worked(it)) {
+                    // without codes there is one such step, the last: it has landed, the workers clear it
+                    if (!of_q)
+                        mbar_arrive(&tail);
                     ok = mbar_wait_bounded(&ready[of_q ? b : 0], of_q ? (it >> 1) & 1 : 0, c.status);
+                }
                 if (!ok)
                     break;
                 tc_fence_after();
@@ -1160,8 +1164,10 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
                 load_scales();
                 load_tokens(it + 4);
                 const int slot = it % stages, b = it & 1;
-                if (!mbar_wait_bounded(&full[slot], (it / stages) & 1, c.status) ||
-                    (it >= 2 && !mbar_wait_bounded(&taken[b], ((it >> 1) & 1) ^ 1, c.status)) || aborted(&abort_flag)) {
+                // first the buffer: the MMAs of step it - 2, and so those of the slot's last use, are done,
+                // and full can only be in the phase that this step ends (a group sees every other one)
+                if ((it >= 2 && !mbar_wait_bounded(&taken[b], ((it >> 1) & 1) ^ 1, c.status)) ||
+                    !mbar_wait_bounded(&full[slot], (it / stages) & 1, c.status) || aborted(&abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -1203,7 +1209,9 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
         } else if (n_st > 0 && rows_of(n_st - 1) < 64) {
             // the adapter's last step: zeros past its last token
             const int it = n_st - 1, slot = it % stages, r0 = rows_of(it);
-            ok = mbar_wait_bounded(&full[slot], (it / stages) & 1, c.status);
+            // told by the MMA thread, which follows every phase of the ring (a wait for one phase of full
+            // alone would take an earlier one of the same parity for it)
+            ok = mbar_wait_bounded(&tail, 0, c.status);
             if (ok) {
                 const uint32_t s0 = smem_u32(S(slot));
                 for (int e = w * 32 + lane; e < (64 - r0) * 32 && w < kGramWork / 2; e += kGramWork * 16)
@@ -1527,7 +1535,7 @@ bool few_tokens(const AdapterFwdArgs& a)
     // 18 clusters of 8 at a time, each reading its adapter once
     const double one = 3 + std::ceil(tiles(kTileS) / 18) * 1.4e-5 * rank_up(a.R) * row;
     const double two = 8 + 4e-4 * longer + tiles(kTileL) * row * 5e-5;
-    return one < two;
+    return one < two && max_tiles(a.M, a.L, kTileS) <= 65535;  // a grid's y
 }
 
 template <typename T>

@@ -49,7 +49,9 @@
  *     completed.  The activation quantiser of a w8a8 / w4a8 call of more
  *     than 16 tokens is itself a programmatic dependent: it waits for its
  *     predecessors before it reads x or writes anything, but it does not
- *     end the run.  (The activation quantiser and the preparation kernel let
+ *     end the run; neither do qlin_adapters_forward, qlin_adapters_backward
+ *     and pergroup_wgrad, whose kernels read and write only after their
+ *     wait.  (The activation quantiser and the preparation kernel let
  *     the second kernel of their own call start early: it fetches the call's
  *     weights meanwhile and reads the quantiser's or preparation's output
  *     only after its wait.)
@@ -364,16 +366,18 @@ size_t qlin_adapters_workspace_size(int64_t M, int64_t N, int64_t K, int64_t L, 
  * Adapters, forward.  x: [M, K]; a: [L, R, K] and b: [L, N, R], the factors of
  * every adapter (a rank below R: zero rows of a_i, zero columns of b_i);
  * scales: fp32 [L]; base: [M, N] or NULL (zeros); out: [M, N], may be base
- * itself (no other overlap); all of dtype dt.  plan: of the same M and L.
+ * itself (no other overlap: QLIN_ERR_INVALID_ARG for out over x or u); all of
+ * dtype dt, aligned to their elements.  plan: of the same M and L.
  * u: fp32 [M, R] or NULL: gets A_i x[m], zero without an adapter -- what the
  * backward pass needs.  1 <= R <= 128; K, N < 2^21 (QLIN_ERR_UNSUPPORTED
  * otherwise).  Accumulation in fp32, u split into two 16-bit halves (a
  * relative error of 2^-16 at most) for the second product, one rounding of
- * the sum to dt.  fp32, and R, K or N that is not a multiple of 8, or tensors
- * that are not 16-byte aligned, take slower kernels.  workspace:
+ * the sum to dt.  bf16 and fp16 with R, K and N multiples of 8 and tensors
+ * aligned to 16 bytes run on the tensor cores: few tokens in one launch, more
+ * in two.  Everything else takes general fp32 kernels (slower).  workspace:
  * qlin_adapters_workspace_size(M, N, K, L, R, 0) bytes, 256-byte aligned.
- * Results do not depend on the order of other requests' tokens in the batch
- * beyond rounding, and are the same from run to run.
+ * What a token or an adapter holds that is not finite reaches only its own
+ * adapter's tokens and gradients.  Results are the same from run to run.
  */
 qlin_status qlin_adapters_forward(const void* x, qlin_dtype dt, int64_t M, int64_t K, const void* a, const void* b,
                                   const float* scales, int64_t L, int64_t R, int64_t N, const void* plan,

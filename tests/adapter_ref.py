@@ -85,6 +85,9 @@ def make_ids(kind, M, L, gen):
         return torch.full((M,), -1, dtype=torch.int32, device="cuda")
     if kind == "one":
         return torch.full((M,), L - 1, dtype=torch.int32, device="cuda")
+    if kind == "blocks":  # long runs: tiles of consecutive tokens, and some that are not
+        return torch.randint(0, L, (M // 300 + 1,), generator=gen, device="cuda", dtype=torch.int32)[
+            torch.arange(M, device="cuda") // 300].contiguous()
     if kind == "outside":  # what is not an adapter is none
         ids = torch.randint(-3, L + 3, (M,), generator=gen, device="cuda", dtype=torch.int32)
         ids[0] = 2 ** 31 - 1

@@ -27,6 +27,12 @@ CASES = [
     (BF, 300, 1032, 520, 6, 72, "outside"), (BF, 777, 512, 640, 12, 32, "random"), (HF, 1000, 640, 384, 2, 96, "runs"),
     (BF, 1531, 1024, 1288, 3, 16, "random"), (BF, 2049, 512, 512, 4, 64, "runs"), (HF, 513, 4096, 256, 40, 16, "runs"),
     (BF, 640, 256, 5000, 2, 128, "even"),
+    # many steps of an adapter's tokens through the rings, the last one short: consecutive and scattered
+    (BF, 2500, 256, 264, 1, 16, "one"), (BF, 2531, 512, 520, 2, 64, "blocks"), (HF, 3001, 256, 136, 2, 128, "blocks"),
+    (BF, 2600, 256, 264, 1, 24, "random"), (HF, 1923, 768, 264, 1, 8, "one"),
+    # one column block, many adapters, 16-way and no split of the first product, fp16 above rank 64
+    (BF, 70, 8, 8, 2, 8, "random"), (BF, 1500, 64, 128, 1000, 8, "random"), (HF, 260, 8192, 136, 1, 24, "one"),
+    (BF, 9000, 128, 72, 3, 16, "runs"), (HF, 333, 1016, 4104, 5, 104, "runs"), (BF, 24, 4096, 4096, 2, 128, "random"),
     # sizes that are not multiples of 8, rank 1, fp32
     (BF, 5, 100, 60, 2, 4, "random"), (HF, 33, 77, 131, 3, 1, "random"), (BF, 130, 515, 258, 2, 12, "runs"),
     (F32, 1, 256, 264, 2, 16, "one"), (F32, 65, 300, 130, 3, 5, "random"), (F32, 200, 1024, 512, 4, 64, "outside"),
@@ -311,3 +317,67 @@ def test_refusals(ql):
                              dx_base=d["dx_base"])
     with pytest.raises(ql.QlinError):
         ql.adapters_plan(torch.zeros(0, dtype=torch.int32, device="cuda"), 2)
+
+
+@pytest.mark.parametrize("case", [(BF, 300, 256, 264, 3, 16, "runs"), (HF, 5, 128, 136, 2, 8, "random")], ids=name)
+def test_tensors_aligned_to_their_elements_only(ql, case):
+    """Contiguous tensors that begin one element past a 16-byte boundary take the general kernels."""
+    d = ref.make(case)
+    M, K, N, L, R = case[1:6]
+
+    def shifted(t):
+        flat = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+        return flat[1:].view(t.shape).copy_(t)
+
+    for k in ("x", "a", "b", "base", "dy", "dx_base"):
+        d[k] = shifted(d[k])
+    plan = ql.adapters_plan(d["ids"], L)
+    u = shifted(torch.zeros(M, R, device="cuda"))
+    out = ql.adapters_forward(d["x"], d["a"], d["b"], d["scales"], plan, base=d["base"], u=u)
+    ref.check_forward(d["x"], d["a"], d["b"], d["scales"], d["ids"], d["base"], out, u)
+    dx, da, db = ql.adapters_backward(d["dy"], d["a"], d["b"], d["scales"], plan, u, x=d["x"], dx_base=d["dx_base"])
+    ref.check_backward(d["dy"], d["a"], d["b"], d["scales"], d["ids"], u, d["x"].double(), d["dx_base"], dx, da, db,
+                       False)
+
+
+def test_one_plan_serves_layers_of_other_sizes(ql):
+    """A plan depends on the batch alone: projections of other sizes, ranks and types, forward and backward."""
+    first = ref.make((BF, 260, 256, 512, 4, 16, "runs"))
+    plan = ql.adapters_plan(first["ids"], 4)
+    for case in ((BF, 260, 512, 128, 4, 32, "runs"), (HF, 260, 128, 640, 4, 8, "runs"), (F32, 260, 64, 72, 4, 3, "runs")):
+        d = ref.make(case, seed=7)
+        d["ids"] = first["ids"]
+        u = torch.empty(260, case[5], device="cuda")
+        out = ql.adapters_forward(d["x"], d["a"], d["b"], d["scales"], plan, base=d["base"], u=u)
+        ref.check_forward(d["x"], d["a"], d["b"], d["scales"], d["ids"], d["base"], out, u)
+        dx, da, db = ql.adapters_backward(d["dy"], d["a"], d["b"], d["scales"], plan, u, x=d["x"])
+        ref.check_backward(d["dy"], d["a"], d["b"], d["scales"], d["ids"], u, d["x"].double(), None, dx, da, db, False)
+
+
+def test_between_layer_calls_of_one_run(ql):
+    """Layer, adapters, layer, adapters with no other operation between: the library's kernels start early behind
+    one another, and each reads what the one before wrote."""
+    K, N, L, R, M = 512, 512, 3, 16, 6
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    codes, sc, bi = ql.quantize(torch.randn(N, K, generator=gen, device="cuda") * 0.05, 4, 64)
+    d = ref.make((BF, M, K, N, L, R, "random"))
+    plan = ql.adapters_plan(d["ids"], L)
+    ws = torch.empty(ql.adapters_workspace_size(M, N, K, L, R), dtype=torch.uint8, device="cuda")
+    y, z = torch.empty(M, N, dtype=BF, device="cuda"), torch.empty(M, N, dtype=BF, device="cuda")
+    results = []
+    for _ in range(30):
+        ql.matmul(d["x"], codes, sc, bi, 4, 64, out=y)
+        ql.adapters_forward(d["x"], d["a"], d["b"], d["scales"], plan, base=y, out=y, workspace=ws)
+        ql.matmul(y, codes, sc, bi, 4, 64, out=z)
+        ql.adapters_forward(y, d["a"], d["b"], d["scales"], plan, base=z, out=z, workspace=ws)
+        results.append(z.clone())
+    base = ql.matmul(d["x"], codes, sc, bi, 4, 64)
+    torch.cuda.synchronize()
+    mid = ql.adapters_forward(d["x"], d["a"], d["b"], d["scales"], plan, base=base)
+    torch.cuda.synchronize()
+    ref.check_forward(d["x"], d["a"], d["b"], d["scales"], d["ids"], base, mid)
+    last = ql.matmul(mid, codes, sc, bi, 4, 64)
+    torch.cuda.synchronize()
+    want = ql.adapters_forward(mid, d["a"], d["b"], d["scales"], plan, base=last)
+    assert all(torch.equal(r, want) for r in results)
+    assert ql.device_status() == ql.QLIN_OK
