@@ -92,11 +92,11 @@ cudaError_t launch_adapters_forward_simt(const AdapterFwdArgs& a, cudaStream_t s
 cudaError_t launch_adapters_backward_simt(const AdapterBwdArgs& a, cudaStream_t st);
 
 
-// Tensor-core kernels (k_adapters_tc.cu): bf16 and fp16, R, K and N multiples of 8, every tensor
+// Tensor-core kernels (k_adapters_tc.cu): bf16 and fp16, K and N multiples of 8, R of 4, every tensor
 // 16-byte aligned.
 bool adapters_tc_takes(const AdapterFwdArgs& a);
 bool adapters_tc_takes(const AdapterBwdArgs& a);
-size_t adapters_tc_workspace(int64_t M, int64_t L, int64_t R);
+size_t adapters_tc_workspace(int64_t M, int64_t N, int64_t L, int64_t R);
 cudaError_t launch_adapters_forward_tc(const AdapterFwdArgs& a, cudaStream_t st, const DeviceInfo& dev);
 cudaError_t launch_adapters_backward_tc(const AdapterBwdArgs& a, cudaStream_t st, const DeviceInfo& dev);
 

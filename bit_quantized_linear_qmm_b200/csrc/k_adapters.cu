@@ -7,7 +7,7 @@
 //
 // The general kernels are six instances of one 64 x 64 fp32 tile product (4 x 4 outputs a thread,
 // operands staged in shared memory).  They serve fp32, whose products the 16-bit tensor cores do
-// not hold, and ranks and row lengths that are not multiples of 8 elements.  Sums run in fp32, in
+// not hold, row lengths that are not multiples of 8 elements, odd ranks.  Sums run in fp32, in
 // a fixed order: partial sums of 128 terms are added to a second accumulator, so that the rounding
 // error grows with the number of partial sums and not of terms.
 #include "adapters.cuh"

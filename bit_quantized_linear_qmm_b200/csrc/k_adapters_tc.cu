@@ -106,6 +106,8 @@ struct Common {
     PlanView plan;
     int64_t M, slots;       // slots: 128 for each tile of the plan's bound
     int L, R, Rq;
+    int Rb;                 // ranks of a row of B as the tensor maps read it
+    void* b_pad;            // where R % 8 is 4: B with rows of Rb = R + 4 ranks
     uint16_t* row_halves;   // [2][slots][Rq]: hi and lo of h (forward) or v, for the wide product
     uint16_t* v_halves;     // [2][slots][Rq]: of v for the grams (bf16: the same)
     uint16_t* u_halves;     // [2][slots][Rq]: of u for the grams
@@ -1320,6 +1322,23 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
         tmem_dealloc(tmem, (uint32_t)p.tmem_cols);
 }
 
+// ------------------------------------------------------------------------------------ pad
+
+// B with its rows widened to a multiple of 8 ranks by zeros (a tensor map's rows are multiples of 16
+// bytes): [rows][4 per] from [rows][R], 8 bytes a thread.
+__global__ void __launch_bounds__(256) adapters_pad_kernel(const uint2* __restrict__ b, uint2* __restrict__ out, int64_t rows,
+                                                           int r4, int per)
+{
+    pdl_launch_dependents();
+    pdl_wait_prior_grids();
+    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (e >= rows * per)
+        return;
+    const int64_t row = e / per;
+    const int c = (int)(e - row * per);
+    out[e] = c < r4 ? __ldg(b + row * r4 + c) : make_uint2(0u, 0u);
+}
+
 // ------------------------------------------------------------------------------------ host
 
 bool a16(std::initializer_list<const void*> ps)
@@ -1341,21 +1360,23 @@ uint32_t tmem_columns(int n)
 
 // The workspace: halves for the wide product, halves of v and u for the grams, and what fp16 needs.
 struct Layout {
-    size_t halves, back, v, tile_max, total;
-    Layout(int64_t M, int64_t L, int64_t R)
+    size_t halves, back, v, tile_max, pad, total;
+    Layout(int64_t M, int64_t N, int64_t L, int64_t R)
     {
         const size_t tiles = (size_t)max_tiles(M, L, kTileL), slots = tiles * kTileL;
         halves = up256(2 * slots * (size_t)rank_up(R) * 2);
         back = up256(slots * sizeof(float));
         v = up256(slots * (size_t)rank_up(R) * sizeof(float));
         tile_max = up256(tiles * kMaxSplit * 2 * sizeof(float));
-        total = 3 * halves + back + v + tile_max;
+        pad = R % 8 ? up256((size_t)L * (size_t)N * (size_t)(R + 4) * 2) : 0;
+        total = 3 * halves + back + v + tile_max + pad;
     }
 };
 
-Common common_of(const PlanView& plan, qlin_dtype dt, int64_t M, int64_t L, int64_t R, void* ws, const DeviceInfo& dev)
+Common common_of(const PlanView& plan, qlin_dtype dt, int64_t M, int64_t N, int64_t L, int64_t R, void* ws,
+                 const DeviceInfo& dev)
 {
-    const Layout l(M, L, R);
+    const Layout l(M, N, L, R);
     uint8_t* p = static_cast<uint8_t*>(ws);
     Common c;
     c.plan = plan;
@@ -1364,6 +1385,8 @@ Common common_of(const PlanView& plan, qlin_dtype dt, int64_t M, int64_t L, int6
     c.L = (int)L;
     c.R = (int)R;
     c.Rq = rank_up(R);
+    c.Rb = (int)((R + 7) / 8 * 8);
+    c.b_pad = p + 3 * l.halves + l.back + l.v + l.tile_max;
     c.row_halves = reinterpret_cast<uint16_t*>(p);
     c.v_halves = dt == QLIN_F16 ? reinterpret_cast<uint16_t*>(p + l.halves) : c.row_halves;
     c.u_halves = reinterpret_cast<uint16_t*>(p + 2 * l.halves);
@@ -1449,7 +1472,7 @@ cudaError_t launch_narrow(const Common& c, const void* w, int64_t K, const void*
     // a factor of box rows: forward Rq rows of 64 k; backward 64 rows of 64 ranks, an atom each
     if (!row_maps(p.w, tm_type<T>(), 2, w, c.M, K) ||
         !(FWD ? encode_tmap_3d(&p.tm_f, tm_type<T>(), f, (uint64_t)K, (uint64_t)c.R, (uint64_t)c.L, 2, 64, (uint32_t)c.Rq)
-              : encode_tmap_3d(&p.tm_f, tm_type<T>(), f, (uint64_t)c.R, (uint64_t)K, (uint64_t)c.L, 2, 64, 64)))
+              : encode_tmap_3d(&p.tm_f, tm_type<T>(), f, (uint64_t)c.Rb, (uint64_t)K, (uint64_t)c.L, 2, 64, 64)))
         return cudaErrorInvalidValue;
     p.f_bytes = FWD ? c.Rq * 128 : (c.Rq + 63) / 64 * (int)kAtom;
     const int stage = 2 * (int)kAtom + p.f_bytes;
@@ -1477,7 +1500,7 @@ cudaError_t launch_wide(const Common& c, const void* f, const float* scales, con
     p.out = out;
     p.N = N;
     if (!row_maps(p.base, tm_type<T>(), 2, base ? base : out, c.M, N) || !half_map<T>(p.tm_h, c, c.row_halves, 128) ||
-        !(FWD ? encode_tmap_3d(&p.tm_f, tm_type<T>(), f, (uint64_t)c.R, (uint64_t)N, (uint64_t)c.L, 2, 64, kWideCols)
+        !(FWD ? encode_tmap_3d(&p.tm_f, tm_type<T>(), f, (uint64_t)c.Rb, (uint64_t)N, (uint64_t)c.L, 2, 64, kWideCols)
               : encode_tmap_3d(&p.tm_f, tm_type<T>(), f, (uint64_t)N, (uint64_t)c.R, (uint64_t)c.L, 2, 64, (uint32_t)c.Rq)))
         return cudaErrorInvalidValue;
     const int atoms = (c.Rq + 63) / 64, h = 2 * atoms * 2 * (int)kAtom;
@@ -1566,21 +1589,48 @@ cudaError_t launch_decode(const Common& c, const AdapterFwdArgs& a, cudaStream_t
     return launch(adapters_decode_kernel<T, 8>, grid, th, smem(8), z, p, st);
 }
 
+// B as the tensor maps can read it: itself, or its padded copy in the workspace.
+cudaError_t map_rows(const Common& c, const void* b, int64_t N, cudaStream_t st, const void*& rows)
+{
+    rows = b;
+    if (c.R % 8 == 0)
+        return cudaSuccess;
+    rows = c.b_pad;
+    const int64_t n = (int64_t)c.L * N, per = c.Rb / 4;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((n * per + 255) / 256));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, adapters_pad_kernel, static_cast<const uint2*>(b), static_cast<uint2*>(c.b_pad), n,
+                              c.R / 4, (int)per);
+}
+
 template <typename T>
 cudaError_t forward_t(const AdapterFwdArgs& a, cudaStream_t st, const DeviceInfo& dev)
 {
-    const Common c = common_of(a.plan, a.dt, a.M, a.L, a.R, a.ws, dev);
+    const Common c = common_of(a.plan, a.dt, a.M, a.N, a.L, a.R, a.ws, dev);
     if (few_tokens(a))
         return launch_decode<T>(c, a, st);
-    const cudaError_t e = launch_narrow<T, true>(c, a.x, a.K, a.a, nullptr, nullptr, a.u, st, dev);
-    return e != cudaSuccess ? e : launch_wide<T, true>(c, a.b, a.scales, a.base, a.out, a.N, st, dev);
+    const void* b;
+    cudaError_t e = map_rows(c, a.b, a.N, st, b);
+    if (e == cudaSuccess)
+        e = launch_narrow<T, true>(c, a.x, a.K, a.a, nullptr, nullptr, a.u, st, dev);
+    return e != cudaSuccess ? e : launch_wide<T, true>(c, b, a.scales, a.base, a.out, a.N, st, dev);
 }
 
 template <typename T>
 cudaError_t backward_t(const AdapterBwdArgs& a, cudaStream_t st, const DeviceInfo& dev)
 {
-    const Common c = common_of(a.plan, a.dt, a.M, a.L, a.R, a.ws, dev);
-    cudaError_t e = launch_narrow<T, false>(c, a.dy, a.N, a.b, a.scales, a.u, nullptr, st, dev);
+    const Common c = common_of(a.plan, a.dt, a.M, a.N, a.L, a.R, a.ws, dev);
+    const void* b;
+    cudaError_t e = map_rows(c, a.b, a.N, st, b);
+    if (e == cudaSuccess)
+        e = launch_narrow<T, false>(c, a.dy, a.N, b, a.scales, a.u, nullptr, st, dev);
     if (e == cudaSuccess && Is16<T>::f16) {
         const SplitParams p = {c, a.u, narrow_split(c, a.N)};
         e = launch(adapters_split_kernel, dim3((unsigned)max_tiles(a.M, a.L, kTileL)), 256, 0, 0, p, st);
@@ -1595,7 +1645,7 @@ cudaError_t backward_t(const AdapterBwdArgs& a, cudaStream_t st, const DeviceInf
 bool tc_sizes(qlin_dtype dt, int64_t M, int64_t N, int64_t K, int64_t L, int64_t R)
 {
     // the tile list and the gram jobs are a grid's y
-    return dt != QLIN_F32 && R % 8 == 0 && K % 8 == 0 && N % 8 == 0 && max_tiles(M, L, kTileL) <= 65535 &&
+    return dt != QLIN_F32 && R % 4 == 0 && K % 8 == 0 && N % 8 == 0 && max_tiles(M, L, kTileL) <= 65535 &&
            L * ((N + 255) / 256 + (K + 255) / 256) <= 65535;
 }
 
@@ -1611,7 +1661,7 @@ bool adapters_tc_takes(const AdapterBwdArgs& a)
            a16({a.dy, a.a, a.b, a.u, a.x, a.q, a.dx_base, a.dx, a.da, a.db});
 }
 
-size_t adapters_tc_workspace(int64_t M, int64_t L, int64_t R) { return Layout(M, L, R).total; }
+size_t adapters_tc_workspace(int64_t M, int64_t N, int64_t L, int64_t R) { return Layout(M, N, L, R).total; }
 
 cudaError_t launch_adapters_forward_tc(const AdapterFwdArgs& a, cudaStream_t st, const DeviceInfo& dev)
 {

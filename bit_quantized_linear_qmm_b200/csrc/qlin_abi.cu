@@ -589,7 +589,7 @@ size_t qlin_adapters_workspace_size(int64_t M, int64_t N, int64_t K, int64_t L, 
     if (check_plan(M, L) != QLIN_OK || N <= 0 || K <= 0 || R <= 0 || R > kMaxRank || N >= kMaxFeatures ||
         K >= kMaxFeatures)
         return 0;
-    const size_t simt = align256(adapters_simt_workspace(M, N, K, R)), tc = align256(adapters_tc_workspace(M, L, R));
+    const size_t simt = align256(adapters_simt_workspace(M, N, K, R)), tc = align256(adapters_tc_workspace(M, N, L, R));
     return simt > tc ? simt : tc;
 }
 

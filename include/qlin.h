@@ -372,7 +372,7 @@ size_t qlin_adapters_workspace_size(int64_t M, int64_t N, int64_t K, int64_t L, 
  * backward pass needs.  1 <= R <= 128; K, N < 2^21 (QLIN_ERR_UNSUPPORTED
  * otherwise).  Accumulation in fp32, u split into two 16-bit halves (a
  * relative error of 2^-16 at most) for the second product, one rounding of
- * the sum to dt.  bf16 and fp16 with R, K and N multiples of 8 and tensors
+ * the sum to dt.  bf16 and fp16 with K and N multiples of 8, R of 4 and tensors
  * aligned to 16 bytes run on the tensor cores: few tokens in one launch, more
  * in two.  Everything else takes general fp32 kernels (slower).  workspace:
  * qlin_adapters_workspace_size(M, N, K, L, R, 0) bytes, 256-byte aligned.

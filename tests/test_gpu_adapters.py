@@ -30,6 +30,9 @@ CASES = [
     # many steps of an adapter's tokens through the rings, the last one short: consecutive and scattered
     (BF, 2500, 256, 264, 1, 16, "one"), (BF, 2531, 512, 520, 2, 64, "blocks"), (HF, 3001, 256, 136, 2, 128, "blocks"),
     (BF, 2600, 256, 264, 1, 24, "random"), (HF, 1923, 768, 264, 1, 8, "one"),
+    # ranks of 4 modulo 8: rows of b that no tensor map takes
+    (BF, 300, 256, 264, 3, 12, "runs"), (HF, 5, 128, 136, 2, 4, "random"), (HF, 700, 264, 512, 4, 4, "runs"),
+    (BF, 900, 512, 264, 2, 68, "blocks"),
     # one column block, many adapters, 16-way and no split of the first product, fp16 above rank 64
     (BF, 70, 8, 8, 2, 8, "random"), (BF, 1500, 64, 128, 1000, 8, "random"), (HF, 260, 8192, 136, 1, 24, "one"),
     (BF, 9000, 128, 72, 3, 16, "runs"), (HF, 333, 1016, 4104, 5, 104, "runs"), (BF, 24, 4096, 4096, 2, 128, "random"),
