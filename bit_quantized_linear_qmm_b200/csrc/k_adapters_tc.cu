@@ -1537,9 +1537,11 @@ cudaError_t launch_grams(const Common& c, const AdapterBwdArgs& a, cudaStream_t 
         return cudaErrorInvalidValue;
     p.room = 224 * 1024;
     const int64_t jobs = (int64_t)c.L * (p.strips_y + p.strips_x);
-    // split an adapter's tokens until every SM has work, at least two steps each on average
+    // split an adapter's tokens over z CTAs, at least two steps each on average, as long as all clusters
+    // run at once: with one CTA an SM a GPC of 18 holds 9, 4 or 2 clusters of 2, 4 or 8.  More are slower:
+    // 32 jobs (4096 tokens of one adapter, 4096 x 4096) 61 us in all by 4, 82 by 8; 64 jobs 46 by 2, 60 by 4
     int z = 1;
-    while (z < kMaxGramSplit && jobs * z < dev.sm_count && c.M / c.L / 64 >= 4 * z)
+    while (z < kMaxGramSplit && jobs <= (z == 1 ? 72 : z == 2 ? 32 : 16) && c.M / c.L / 64 >= 4 * z)
         z *= 2;
     return launch(adapters_gram_kernel<T>, dim3((unsigned)z, (unsigned)jobs), kGramThreads, p.room + 1024, z, p, st);
 }
