@@ -6,7 +6,7 @@
 //              dA_i = sum_m v[m] x[m]^T   dB_i = s_i sum_m dy[m] u[m]^T        over the tokens of i
 //
 // The general kernels are six instances of one 64 x 64 fp32 tile product (4 x 4 outputs a thread,
-// operands staged in shared memory).  They serve fp32, whose products the 16-bit tensor cores do
+// operands staged in shared memory; 64 x 32 or 64 x 16 where the second side is a lower rank).  They serve fp32, whose products the 16-bit tensor cores do
 // not hold, row lengths that are not multiples of 8 elements, odd ranks.  Sums run in fp32, in
 // a fixed order: partial sums of 128 terms are added to a second accumulator, so that the rounding
 // error grows with the number of partial sums and not of terms.
@@ -147,7 +147,7 @@ QLIN_DEV bool sub_tile(const PlanView& v, bool with_none, SubTile& s)
 
 // part[z][position][r] = the z-th part of sum_k w[token][k] f_i[r][k]; w = x, f = A (forward: the
 // factor's rows run along k) or w = dy, f = B^T (backward: along r).
-template <typename T, bool FWD>
+template <typename T, bool FWD, int C>
 __global__ void __launch_bounds__(kThreads) adapters_narrow_kernel(const T* __restrict__ w, const T* __restrict__ f,
                                                                    int64_t M, int64_t K, int R, PlanView v,
                                                                    float* __restrict__ part)
@@ -155,13 +155,13 @@ __global__ void __launch_bounds__(kThreads) adapters_narrow_kernel(const T* __re
     SubTile s;
     if (!sub_tile(v, false, s))
         return;
-    const int r0 = blockIdx.y * kB;
+    const int r0 = blockIdx.y * (16 * C);
     const int64_t per = ((K + gridDim.z - 1) / gridDim.z + kBK - 1) / kBK * kBK;
     const int64_t k0 = per * blockIdx.z, k1 = k0 + per < K ? k0 + per : K;
     const T* fi = f + (size_t)s.adapter * R * K;
     const int* perm = v.perm + s.start;
-    float o[4][4];
-    tile_product<true, FWD>(
+    float o[4][C];
+    tile_product<C, true, FWD>(
         k0, k1, [&](int i, int64_t k) { return i < s.count ? to_float(w[(size_t)perm[i] * K + k]) : 0.f; },
         [&](int j, int64_t k) {
             return r0 + j < R ? to_float(FWD ? fi[(size_t)(r0 + j) * K + k] : fi[(size_t)k * R + r0 + j]) : 0.f;
@@ -171,9 +171,9 @@ __global__ void __launch_bounds__(kThreads) adapters_narrow_kernel(const T* __re
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-            if (4 * ty + r < s.count && r0 + 4 * tx + c < R)
-                part[((size_t)blockIdx.z * M + s.start + 4 * ty + r) * R + r0 + 4 * tx + c] = o[r][c];
+        for (int c = 0; c < C; ++c)
+            if (4 * ty + r < s.count && r0 + C * tx + c < R)
+                part[((size_t)blockIdx.z * M + s.start + 4 * ty + r) * R + r0 + C * tx + c] = o[r][c];
 }
 
 // sum[position][r] = sum over the parts, in order; u (forward, [token][r]) gets the same, and zero
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kThreads) adapters_wide_kernel(const float* __
     if (has) {
         const T* fi = f + (size_t)s.adapter * R * N;
         const float sc = FWD ? scales[s.adapter] : 1.f;
-        tile_product<true, FWD>(
+        tile_product<4, true, FWD>(
             0, R, [&](int i, int64_t r) { return i < s.count ? sc * h[(size_t)(s.start + i) * R + r] : 0.f; },
             [&](int j, int64_t r) {
                 return n0 + j < N ? to_float(FWD ? fi[(size_t)(n0 + j) * R + r] : fi[(size_t)r * N + n0 + j]) : 0.f;
@@ -251,35 +251,35 @@ struct Input {
 };
 
 // dA_i[r][k] = sum over the tokens of i of v[position][r] x[token][k]; zero without tokens.
-template <typename T>
+template <typename T, int C>
 __global__ void __launch_bounds__(kThreads) adapters_da_kernel(const float* __restrict__ h, Input<T> x,
                                                                T* __restrict__ da, int64_t K, int R, PlanView v)
 {
-    const int i = blockIdx.z, r0 = blockIdx.y * kB;
+    const int i = blockIdx.z, r0 = blockIdx.y * (16 * C);
     const int64_t c0 = (int64_t)blockIdx.x * kB;
-    float o[4][4];
-    tile_product<false, false>(
-        v.seg[i], v.seg[i + 1], [&](int r, int64_t p) { return r0 + r < R ? h[(size_t)p * R + r0 + r] : 0.f; },
-        [&](int c, int64_t p) { return c0 + c < K ? x(v.perm[p], c0 + c) : 0.f; }, o);
+    float o[4][C];
+    tile_product<C, false, false>(
+        v.seg[i], v.seg[i + 1], [&](int k, int64_t p) { return c0 + k < K ? x(v.perm[p], c0 + k) : 0.f; },
+        [&](int r, int64_t p) { return r0 + r < R ? h[(size_t)p * R + r0 + r] : 0.f; }, o);
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-            if (r0 + 4 * ty + r < R && c0 + 4 * tx + c < K)
-                da[((size_t)i * R + r0 + 4 * ty + r) * K + c0 + 4 * tx + c] = from_float<T>(o[r][c]);
+        for (int r = 0; r < 4; ++r)
+            if (r0 + C * tx + c < R && c0 + 4 * ty + r < K)
+                da[((size_t)i * R + r0 + C * tx + c) * K + c0 + 4 * ty + r] = from_float<T>(o[r][c]);
 }
 
 // dB_i[n][r] = s_i sum over the tokens of i of dy[token][n] u[token][r]; zero without tokens.
-template <typename T>
+template <typename T, int C>
 __global__ void __launch_bounds__(kThreads) adapters_db_kernel(const T* __restrict__ dy, const float* __restrict__ u,
                                                                const float* __restrict__ scales, T* __restrict__ db,
                                                                int64_t N, int R, PlanView v)
 {
-    const int i = blockIdx.z, r0 = blockIdx.y * kB;
+    const int i = blockIdx.z, r0 = blockIdx.y * (16 * C);
     const int64_t n0 = (int64_t)blockIdx.x * kB;
-    float o[4][4];
-    tile_product<false, false>(
+    float o[4][C];
+    tile_product<C, false, false>(
         v.seg[i], v.seg[i + 1],
         [&](int n, int64_t p) { return n0 + n < N ? to_float(dy[(size_t)v.perm[p] * N + n0 + n]) : 0.f; },
         [&](int r, int64_t p) { return r0 + r < R ? u[(size_t)v.perm[p] * R + r0 + r] : 0.f; }, o);
@@ -289,9 +289,9 @@ __global__ void __launch_bounds__(kThreads) adapters_db_kernel(const T* __restri
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-            if (n0 + 4 * ty + r < N && r0 + 4 * tx + c < R)
-                db[((size_t)i * N + n0 + 4 * ty + r) * R + r0 + 4 * tx + c] = from_float<T>(any ? sc * o[r][c] : 0.f);
+        for (int c = 0; c < C; ++c)
+            if (n0 + 4 * ty + r < N && r0 + C * tx + c < R)
+                db[((size_t)i * N + n0 + 4 * ty + r) * R + r0 + C * tx + c] = from_float<T>(any ? sc * o[r][c] : 0.f);
 }
 
 // v = s_i h in place: the backward pass's narrow sum holds the scale.
@@ -310,14 +310,15 @@ __global__ void __launch_bounds__(256) adapters_scale_kernel(float* __restrict__
 int parts_of(int64_t K) { return (int)(K / 512 < 1 ? 1 : K / 512 > 16 ? 16 : K / 512); }
 unsigned blocks_of(int64_t n, int64_t per) { return (unsigned)((n + per - 1) / per); }
 
-template <typename T>
-cudaError_t forward_t(const AdapterFwdArgs& a, cudaStream_t st)
+// C: ranks of a tile's side by 16
+template <typename T, int C>
+cudaError_t forward_c(const AdapterFwdArgs& a, cudaStream_t st)
 {
     const int R = (int)a.R, L = (int)a.L, parts = parts_of(a.K);
-    const unsigned subs = 2u * (unsigned)max_tiles(a.M, a.L, kTileL), ry = blocks_of(R, kB);
+    const unsigned subs = 2u * (unsigned)max_tiles(a.M, a.L, kTileL), ry = blocks_of(R, 16 * C);
     float* part = static_cast<float*>(a.ws);
     float* sum = part + (size_t)parts * a.M * R;
-    adapters_narrow_kernel<T, true><<<dim3(subs, ry, parts), kThreads, 0, st>>>(
+    adapters_narrow_kernel<T, true, C><<<dim3(subs, ry, parts), kThreads, 0, st>>>(
         static_cast<const T*>(a.x), static_cast<const T*>(a.a), a.M, a.K, R, a.plan, part);
     adapters_sum_kernel<<<blocks_of(a.M * R, 256), 256, 0, st>>>(part, parts, a.M, L, R, a.plan, sum, a.u);
     adapters_wide_kernel<T, true><<<dim3(subs, blocks_of(a.N, kB)), kThreads, 0, st>>>(
@@ -326,14 +327,14 @@ cudaError_t forward_t(const AdapterFwdArgs& a, cudaStream_t st)
     return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t backward_t(const AdapterBwdArgs& a, cudaStream_t st)
+template <typename T, int C>
+cudaError_t backward_c(const AdapterBwdArgs& a, cudaStream_t st)
 {
     const int R = (int)a.R, L = (int)a.L, parts = parts_of(a.N);
-    const unsigned subs = 2u * (unsigned)max_tiles(a.M, a.L, kTileL), ry = blocks_of(R, kB);
+    const unsigned subs = 2u * (unsigned)max_tiles(a.M, a.L, kTileL), ry = blocks_of(R, 16 * C);
     float* part = static_cast<float*>(a.ws);
     float* sum = part + (size_t)parts * a.M * R;
-    adapters_narrow_kernel<T, false><<<dim3(subs, ry, parts), kThreads, 0, st>>>(
+    adapters_narrow_kernel<T, false, C><<<dim3(subs, ry, parts), kThreads, 0, st>>>(
         static_cast<const T*>(a.dy), static_cast<const T*>(a.b), a.M, a.N, R, a.plan, part);
     adapters_sum_kernel<<<blocks_of(a.M * R, 256), 256, 0, st>>>(part, parts, a.M, L, R, a.plan, sum, nullptr);
     adapters_scale_kernel<<<(unsigned)max_tiles(a.M, a.L, kTileL), 256, 0, st>>>(sum, a.scales, L, R, a.plan);
@@ -342,11 +343,22 @@ cudaError_t backward_t(const AdapterBwdArgs& a, cudaStream_t st)
             sum, static_cast<const T*>(a.a), nullptr, static_cast<const T*>(a.dx_base), static_cast<T*>(a.dx), a.K, L,
             R, a.plan);
     const Input<T> in = {static_cast<const T*>(a.x), a.q, a.q_scale, a.g, a.M, a.K};
-    adapters_da_kernel<T><<<dim3(blocks_of(a.K, kB), ry, L), kThreads, 0, st>>>(sum, in, static_cast<T*>(a.da), a.K, R,
-                                                                               a.plan);
-    adapters_db_kernel<T><<<dim3(blocks_of(a.N, kB), ry, L), kThreads, 0, st>>>(
+    adapters_da_kernel<T, C><<<dim3(blocks_of(a.K, kB), ry, L), kThreads, 0, st>>>(sum, in, static_cast<T*>(a.da), a.K,
+                                                                                  R, a.plan);
+    adapters_db_kernel<T, C><<<dim3(blocks_of(a.N, kB), ry, L), kThreads, 0, st>>>(
         static_cast<const T*>(a.dy), a.u, a.scales, static_cast<T*>(a.db), a.N, R, a.plan);
     return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t forward_t(const AdapterFwdArgs& a, cudaStream_t st)
+{
+    return a.R <= 16 ? forward_c<T, 1>(a, st) : a.R <= 32 ? forward_c<T, 2>(a, st) : forward_c<T, 4>(a, st);
+}
+template <typename T>
+cudaError_t backward_t(const AdapterBwdArgs& a, cudaStream_t st)
+{
+    return a.R <= 16 ? backward_c<T, 1>(a, st) : a.R <= 32 ? backward_c<T, 2>(a, st) : backward_c<T, 4>(a, st);
 }
 
 }  // namespace
