@@ -164,6 +164,8 @@ QLIN_DEV int4 row_tokens(const PlanView& v, int start, int count, int i)
 //                columns past the adapter's own are zeros
 //   warp 4       tensor memory, the MMAs (M = 128, N = Rq, K = 16)
 //   warps 5..8   the epilogue
+// dy [4096][14336] at rank 64: 35 us (3.4 TB/s), of which 23 are the steps at 5.1 TB/s and the rest
+// the start, the cluster's sums and their writing; x [777][11008] at rank 32: 14 us.
 constexpr int kLoadWarps = 4;
 constexpr int kNarrowThreads = (kLoadWarps + 1 + 4) * 32;
 constexpr int kNarrowMaxStages = 8;
@@ -477,6 +479,7 @@ __global__ void __launch_bounds__(256) adapters_split_kernel(const SplitParams p
 //                whole 128-byte pieces of a row (base's own place serves as the staging buffer)
 // Tiles of tokens without an adapter pass through without a product (their rows are copied as they
 // are), or are left out when out is base itself.
+// 4096 tokens by 14336 columns at rank 64: 48 us for 235 MB, 4.9 TB/s, 0.75 of the copy rate.
 constexpr int kWideEpi = 8;
 constexpr int kWideThreads = (kLoadWarps + 1 + kWideEpi) * 32;
 constexpr int kWideMaxStages = 4;
@@ -733,6 +736,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapters_wide_kernel(const __
 // a row of A_i or x.  The CTAs split the contraction; each sends its sums [Rq][8] to every CTA of
 // the cluster (one barrier), and takes its share of the 128-column blocks of the second product,
 // whose factor it has prefetched into L2 meanwhile.
+// 1 token, 4096 x 4096, rank 16: 4.1 us (narrow and wide: 10.2); 61 tokens of 32 adapters, 4096 ->
+// 11008: 8.1 us for 23 MB.
 constexpr int kDecodeWarps = 8;
 
 struct DecodeParams {
@@ -963,6 +968,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32) adapters_decode_kernel(cons
 //   warps 5..20  codes: s q in fp32, rounded once to the operand type, into a ring of two buffers;
 //                rows past the adapter's last token: zeros (only there, so what another adapter's
 //                row holds enters no sum); then the epilogue
+// 4096 tokens of 4 adapters, 14336 bf16 columns and 4096 of codes, rank 64: 49 - 56 us by how the
+// tokens fall on the adapters, for 135 MB; a step of 48 KB comes at 62 GB/s an SM.
 constexpr int kGramWork = 16;
 constexpr int kGramThreads = (kLoadWarps + 1 + kGramWork) * 32;
 constexpr int kGramMaxStages = 6;

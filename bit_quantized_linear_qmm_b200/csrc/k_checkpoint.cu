@@ -22,7 +22,8 @@ QLIN_DEV float code_of(uint32_t w, int i) { return (float)(int8_t)(w >> (8 * i))
 
 // Restoring: 1 byte in and 2 or 4 out for each value, bound by memory.  A block takes 8 rows by 512
 // columns (a warp a row), whose scales are neighbours in memory; a thread 8 codes at a time, so that
-// its 16-byte stores (two for fp32) follow one another through the warp.
+// its 16-byte stores (two for fp32) follow one another through the warp.  16384 x 14336 to bf16: 109 us,
+// 6.5 TB/s, the copy rate.
 template <typename T>
 __global__ void __launch_bounds__(256) dequantize_int8_groups_kernel(const int8_t* __restrict__ q,
                                                                      const float* __restrict__ scale, int64_t N,
@@ -89,6 +90,8 @@ __global__ void __launch_bounds__(256) dequantize_int8_groups_kernel(const int8_
 // accumulators' halves, one for a pair.
 // Every wait is bounded; on expiry the kernel records the timeout, every role stops, and TMEM is
 // freed once the MMAs in flight are done.
+// dW [14336][4096] of 4096 tokens: 393 - 453 us by the box's power cap, 1.07 - 1.22 PFLOP/s (single CTAs
+// on 256 x 256 tiles: 501 and more); [4096][11008] of 1000: 93 - 101 us.
 constexpr int kKT = 256;      // inputs k of a tile
 constexpr int kStageM = 64;   // tokens of a stage
 constexpr uint32_t kAtomBytes = 128 * kStageM;
