@@ -25,6 +25,7 @@
 #include <algorithm>
 #include <cmath>
 #include <initializer_list>
+#include <mutex>
 
 #include "adapters.cuh"
 
@@ -1404,18 +1405,37 @@ Common common_of(const PlanView& plan, qlin_dtype dt, int64_t M, int64_t N, int6
     return c;
 }
 
+// Whether this is the first launch of a kernel on the current device: its attributes are set once
+// (0.5 us each), to what any of its launches may need.
+bool first_launch(const void* kern)
+{
+    constexpr int kSlots = 64;  // kernels x devices of this file: 30 on one device
+    static std::mutex mu;
+    static const void* seen[kSlots][8];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 8)
+        return true;
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < kSlots; ++i) {
+        if (seen[i][dev] == kern)
+            return false;
+        if (!seen[i][dev]) {
+            seen[i][dev] = kern;
+            return true;
+        }
+    }
+    return true;
+}
+
 // A launch behind the stream's previous kernel (the kernels wait for it before touching memory),
 // with clusters of cluster_x CTAs along x (0: none).
 template <typename P>
 cudaError_t launch(void (*kern)(const P), dim3 grid, int threads, int smem, int cluster_x, const P& prm, cudaStream_t st)
 {
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess)
-            return e;
-    }
-    if (cluster_x > 8) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if ((smem > 48 * 1024 || cluster_x > 8) && first_launch(reinterpret_cast<const void*>(kern))) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess)
             return e;
     }
@@ -1467,7 +1487,7 @@ int narrow_split(const Common& c, int64_t K)
 }
 
 template <typename T, bool FWD>
-cudaError_t launch_narrow(const Common& c, const void* w, int64_t K, const void* f, const float* scales, const float* u_in,
+cudaError_t launch_narrow(const Common& c, const RowMaps& w, int64_t K, const void* f, const float* scales, const float* u_in,
                           float* u_out, cudaStream_t st, const DeviceInfo& dev)
 {
     NarrowParams p;
@@ -1477,8 +1497,8 @@ cudaError_t launch_narrow(const Common& c, const void* w, int64_t K, const void*
     p.u_in = u_in;
     p.u_out = u_out;
     // a factor of box rows: forward Rq rows of 64 k; backward 64 rows of 64 ranks, an atom each
-    if (!row_maps(p.w, tm_type<T>(), 2, w, c.M, K) ||
-        !(FWD ? encode_tmap_3d(&p.tm_f, tm_type<T>(), f, (uint64_t)K, (uint64_t)c.R, (uint64_t)c.L, 2, 64, (uint32_t)c.Rq)
+    p.w = w;
+    if (!(FWD ? encode_tmap_3d(&p.tm_f, tm_type<T>(), f, (uint64_t)K, (uint64_t)c.R, (uint64_t)c.L, 2, 64, (uint32_t)c.Rq)
               : encode_tmap_3d(&p.tm_f, tm_type<T>(), f, (uint64_t)c.Rb, (uint64_t)K, (uint64_t)c.L, 2, 64, 64)))
         return cudaErrorInvalidValue;
     p.f_bytes = FWD ? c.Rq * 128 : (c.Rq + 63) / 64 * (int)kAtom;
@@ -1522,7 +1542,7 @@ cudaError_t launch_wide(const Common& c, const void* f, const float* scales, con
 }
 
 template <typename T>
-cudaError_t launch_grams(const Common& c, const AdapterBwdArgs& a, cudaStream_t st, const DeviceInfo& dev)
+cudaError_t launch_grams(const Common& c, const AdapterBwdArgs& a, const RowMaps& dy, cudaStream_t st)
 {
     GramParams p;
     p.c = c;
@@ -1537,8 +1557,8 @@ cudaError_t launch_grams(const Common& c, const AdapterBwdArgs& a, cudaStream_t 
     p.db = a.db;
     p.parts = narrow_split(c, a.N);
     p.tmem_cols = 256;
-    if (!row_maps(p.dy, tm_type<T>(), 2, a.dy, c.M, a.N) ||
-        !(a.q ? row_maps(p.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.q, c.M, a.K)
+    p.dy = dy;
+    if (!(a.q ? row_maps(p.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.q, c.M, a.K)
               : row_maps(p.x, tm_type<T>(), 2, a.x, c.M, a.K)) ||
         !half_map<T>(p.tm_u, c, c.u_halves, 64) || !half_map<T>(p.tm_v, c, c.v_halves, 64))
         return cudaErrorInvalidValue;
@@ -1626,9 +1646,12 @@ cudaError_t forward_t(const AdapterFwdArgs& a, cudaStream_t st, const DeviceInfo
     if (few_tokens(a))
         return launch_decode<T>(c, a, st);
     const void* b;
+    RowMaps x;
+    if (!row_maps(x, tm_type<T>(), 2, a.x, a.M, a.K))
+        return cudaErrorInvalidValue;
     cudaError_t e = map_rows(c, a.b, a.N, st, b);
     if (e == cudaSuccess)
-        e = launch_narrow<T, true>(c, a.x, a.K, a.a, nullptr, nullptr, a.u, st, dev);
+        e = launch_narrow<T, true>(c, x, a.K, a.a, nullptr, nullptr, a.u, st, dev);
     return e != cudaSuccess ? e : launch_wide<T, true>(c, b, a.scales, a.base, a.out, a.N, st, dev);
 }
 
@@ -1637,15 +1660,18 @@ cudaError_t backward_t(const AdapterBwdArgs& a, cudaStream_t st, const DeviceInf
 {
     const Common c = common_of(a.plan, a.dt, a.M, a.N, a.L, a.R, a.ws, dev);
     const void* b;
+    RowMaps dy;
+    if (!row_maps(dy, tm_type<T>(), 2, a.dy, a.M, a.N))
+        return cudaErrorInvalidValue;
     cudaError_t e = map_rows(c, a.b, a.N, st, b);
     if (e == cudaSuccess)
-        e = launch_narrow<T, false>(c, a.dy, a.N, b, a.scales, a.u, nullptr, st, dev);
+        e = launch_narrow<T, false>(c, dy, a.N, b, a.scales, a.u, nullptr, st, dev);
     if (e == cudaSuccess && Is16<T>::f16) {
         const SplitParams p = {c, a.u, narrow_split(c, a.N)};
         e = launch(adapters_split_kernel, dim3((unsigned)max_tiles(a.M, a.L, kTileL)), 256, 0, 0, p, st);
     }
     if (e == cudaSuccess)
-        e = launch_grams<T>(c, a, st, dev);
+        e = launch_grams<T>(c, a, dy, st);
     if (e == cudaSuccess && a.dx)
         e = launch_wide<T, false>(c, a.a, nullptr, a.dx_base, a.dx, a.K, st, dev);
     return e;

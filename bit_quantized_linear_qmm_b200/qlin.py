@@ -8,6 +8,7 @@ and filled by the library.  A missing library is an error, never a fallback.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 import re
 from typing import NamedTuple
@@ -347,14 +348,19 @@ def _space(workspace, need: int, dev: int, like):
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
+# the current stream's handle without building a Stream object, 1 us of a call that takes 15
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _run(name, dev: int, *args):
     """Calls a library function on device dev and its current stream."""
     fn = getattr(_lib or lib(), name)
     if torch.cuda.current_device() == dev:
-        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        status = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            status = fn(*args, _raw_stream(dev))
     if status != QLIN_OK:
         _check(status, name)
 
@@ -383,6 +389,7 @@ def adapters_plan(ids, adapters: int, out: AdapterPlan | None = None) -> Adapter
     return out
 
 
+@functools.lru_cache(maxsize=1024)
 def adapters_workspace_size(M: int, N: int, K: int, adapters: int, rank: int, backward: bool = False) -> int:
     return int(lib().qlin_adapters_workspace_size(M, N, K, adapters, rank, int(backward)))
 
@@ -406,7 +413,7 @@ def adapters_forward(x, a, b, scales, plan: AdapterPlan, base=None, out=None, u=
     dt = x.dtype
     if out is None:
         out = x.new_empty((M, N))
-    ws, wp, wn = _space(workspace, lib().qlin_adapters_workspace_size(M, N, K, L, R, 0), dev, x)
+    ws, wp, wn = _space(workspace, adapters_workspace_size(M, N, K, L, R), dev, x)
     _run("qlin_adapters_forward", dev, _fit("x", x, (M, K), dt, dev), _dt(x), M, K, _fit("a", a, (L, R, K), dt, dev),
          _fit("b", b, (L, N, R), dt, dev), _fit("scales", scales, (L,), torch.float32, dev), L, R, N,
          plan.buffer.data_ptr(), plan.buffer.numel(), _fit("base", base, (M, N), dt, dev),
@@ -432,7 +439,7 @@ def adapters_backward(dy, a, b, scales, plan: AdapterPlan, u, x=None, checkpoint
         dx = dy.new_empty((M, K))
     ap, bp = _fit("a", a, (L, R, K), dt, dev), _fit("b", b, (L, N, R), dt, dev)
     da, db = torch.empty_like(a), torch.empty_like(b)
-    ws, wp, wn = _space(workspace, lib().qlin_adapters_workspace_size(M, N, K, L, R, 1), dev, dy)
+    ws, wp, wn = _space(workspace, adapters_workspace_size(M, N, K, L, R, True), dev, dy)
     _run("qlin_adapters_backward", dev, _fit("dy", dy, (M, N), dt, dev), _dt(dy), M, N, ap, bp,
          _fit("scales", scales, (L,), f32, dev), L, R, K, plan.buffer.data_ptr(), plan.buffer.numel(),
          _fit("u", u, (M, R), f32, dev), _fit("x", x, (M, K), dt, dev), _fit("q", q, (M, K), torch.int8, dev),
