@@ -347,7 +347,8 @@ __global__ void __launch_bounds__(kNarrowThreads) adapters_narrow_kernel(const _
         tc_fence_before();
     }
     __syncthreads();
-    cluster_sync();
+    if (z > 1)
+        cluster_sync();
     if (warp > kLoadWarps) {
         // a power of two of lanes takes a row, four columns a lane: 32 / lanes rows a warp at a time
         const float sc = FWD ? 1.f : p.scales[d.adapter];
@@ -412,7 +413,10 @@ __global__ void __launch_bounds__(kNarrowThreads) adapters_narrow_kernel(const _
             }
         }
     }
-    cluster_sync();  // no CTA's shared memory goes while another reads it
+    if (z > 1)
+        cluster_sync();  // no CTA's shared memory goes while another reads it
+    else
+        __syncthreads();
     if (warp == kLoadWarps)
         tmem_dealloc(tmem, (uint32_t)p.tmem_cols);
 }
@@ -1260,7 +1264,8 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
         tc_fence_before();
     }
     __syncthreads();
-    cluster_sync();
+    if (z > 1)
+        cluster_sync();
     if (warp > kLoadWarps) {
         // CTA j adds the cluster's parts of its share of the 256 columns, in order
         const int share = 256 / z, row0 = rank * share;
@@ -1325,7 +1330,8 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
             }
         }
     }
-    cluster_sync();
+    if (z > 1)
+        cluster_sync();
     if (warp == kLoadWarps)
         tmem_dealloc(tmem, (uint32_t)p.tmem_cols);
 }
