@@ -818,8 +818,10 @@ QLIN_DEV float amax16(const uint4 (&u)[2])
 // The same with G/16 lanes per group, 16 consecutive values each (16-byte loads, one 16-byte store
 // of the lane's int8 codes); 16-byte aligned w and q.  A warp takes 8 rows by 512 columns, two rows at
 // a time: lane l of a group divides for row l mod 2 and hands scale and reciprocal to the others, and
-// the 8 scales of a group fill one 32-byte sector.  16384 x 14336 bf16: 135 us, 5.2 TB/s (bound by issue
-// slots, 0.8 of the copy rate).  A code is the low byte of
+// the 8 scales of a group fill one 32-byte sector.  16384 x 14336, g 128: 156 us, 4.6 TB/s for bf16
+// activations whose tokens differ in size; of normal values bf16 183, fp16 142, fp32 178 us (6.6 TB/s).
+// The 16-bit types are bound by issue slots, bf16 most: its short significands meet half-integers more
+// often (4% of a lane's 16 values hold one, 1% in the activations).  A code is the low byte of
 // fma(x, r, 1.5 2^23), the product rounded half to even as rint does it.  With r = (1/s)(1 + e1) the
 // product and the rounded quotient q (1 + e3) differ by less than 2 2^-24 127 = 1.6e-5, so they round
 // alike unless the product lies within 3e-5 of a half-integer; such an element takes the division.
@@ -830,7 +832,7 @@ __global__ void __launch_bounds__(256) quantize_int8_groups_vec_kernel(const TW*
 {
     constexpr int LPG = G / 16;                     // lanes a group
     constexpr int NV = sizeof(TW) == 4 ? 4 : 2;     // 16-byte loads of 16 elements
-    constexpr int RPT = 2;                          // rows at a time (4: 162 us where 2 take 135)
+    constexpr int RPT = 2;                          // rows at a time (4: 185 us where 2 take 156)
     const int lane = threadIdx.x & 31, first = lane & ~(LPG - 1), my = lane & (RPT - 1);
     const int64_t col = (int64_t)blockIdx.x * 512 + 16 * lane;
     const bool in = col < K;  // a group's lanes are all in or all out
