@@ -25,7 +25,6 @@
 #include <algorithm>
 #include <cmath>
 #include <initializer_list>
-#include <mutex>
 
 #include "adapters.cuh"
 
@@ -1411,40 +1410,14 @@ Common common_of(const PlanView& plan, qlin_dtype dt, int64_t M, int64_t N, int6
     return c;
 }
 
-// Whether this is the first launch of a kernel on the current device: its attributes are set once
-// (0.5 us each), to what any of its launches may need.
-bool first_launch(const void* kern)
-{
-    constexpr int kSlots = 64;  // kernels x devices of this file: 30 on one device
-    static std::mutex mu;
-    static const void* seen[kSlots][8];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 8)
-        return true;
-    std::lock_guard<std::mutex> lock(mu);
-    for (int i = 0; i < kSlots; ++i) {
-        if (seen[i][dev] == kern)
-            return false;
-        if (!seen[i][dev]) {
-            seen[i][dev] = kern;
-            return true;
-        }
-    }
-    return true;
-}
-
 // A launch behind the stream's previous kernel (the kernels wait for it before touching memory),
 // with clusters of cluster_x CTAs along x (0: none).
 template <typename P>
 cudaError_t launch(void (*kern)(const P), dim3 grid, int threads, int smem, int cluster_x, const P& prm, cudaStream_t st)
 {
-    if ((smem > 48 * 1024 || cluster_x > 8) && first_launch(reinterpret_cast<const void*>(kern))) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess)
-            return e;
-    }
+    const cudaError_t e = allow_launch(reinterpret_cast<const void*>(kern), smem, cluster_x > 8);
+    if (e != cudaSuccess)
+        return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);

@@ -77,6 +77,49 @@ qlin_status current_device(DeviceInfo& out)
     return slot.state;
 }
 
+cudaError_t allow_launch(const void* kern, int smem, bool wide)
+{
+    if (smem <= 48 * 1024 && !wide)
+        return cudaSuccess;  // what every kernel has
+    struct Entry {
+        const void* kern;
+        int dev, smem;
+        bool wide;
+    };
+    constexpr unsigned kEntries = 4096;  // kernels of the library x devices; without a free one: set each time
+    static Entry entries[kEntries];
+    static std::mutex mu;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const unsigned first = (unsigned)((reinterpret_cast<uintptr_t>(kern) >> 4) * 31u + (unsigned)dev);
+    std::lock_guard<std::mutex> lock(mu);
+    Entry* at = nullptr;
+    for (unsigned i = 0; i < kEntries && !at; ++i) {
+        Entry& s = entries[(first + i) % kEntries];
+        if (!s.kern || (s.kern == kern && s.dev == dev))
+            at = &s;
+    }
+    const bool known = at && at->kern;
+    int had = known ? at->smem : 0;
+    if (!at) {
+        cudaFuncAttributes fa;
+        if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess)
+            return e;
+        had = fa.maxDynamicSharedSizeBytes;
+    }
+    const bool had_wide = known && at->wide;
+    if (smem > had && (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+        return e;
+    if (wide && !had_wide &&
+        (e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+        return e;
+    if (at)
+        *at = {kern, dev, smem > had ? smem : had, wide || had_wide};
+    return cudaSuccess;
+}
+
 namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -326,6 +326,12 @@ struct DeviceInfo {
 // part (QLIN_ERR_DEVICE otherwise); defined in qlin_abi.cu.
 qlin_status current_device(DeviceInfo& out);
 
+// Lets `kern` be launched on the current device with `smem` bytes of dynamic shared memory and, where
+// `wide`, in clusters of more than 8 CTAs.  These limits belong to the kernel and not to a launch:
+// they are only ever raised, and remembered once they are set, so that no other host thread's launch
+// meets a limit that is lower than its own call asked for (qlin_abi.cu).
+cudaError_t allow_launch(const void* kern, int smem, bool wide = false);
+
 // Host: encodes a 2-D tiled tensor map (row-major [dim1][dim0] elements,
 // row pitch `pitch_bytes`) with box {box0, box1}, 128-byte swizzle, zero
 // fill (or the given swizzle).  Returns false if the driver entry point is unavailable or rejects
