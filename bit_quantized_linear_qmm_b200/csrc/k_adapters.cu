@@ -366,8 +366,7 @@ cudaError_t backward_t(const AdapterBwdArgs& a, cudaStream_t st)
 cudaError_t launch_adapters_plan(const int32_t* ids, int64_t M, int64_t L, void* plan, cudaStream_t st)
 {
     const int smem = (int)(32 * (L + 1) * sizeof(int));
-    const cudaError_t e =
-        cudaFuncSetAttribute(adapters_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = allow_launch(reinterpret_cast<const void*>(adapters_plan_kernel), smem);
     if (e != cudaSuccess)
         return e;
     adapters_plan_kernel<<<1, 1024, smem, st>>>(ids, (int)M, (int)L, plan_view(plan, M, L));

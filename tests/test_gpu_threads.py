@@ -40,6 +40,29 @@ def at_once(body):
 streams = [torch.cuda.Stream() for _ in range({threads})]
 """
 
+# calls in a loop without the interpreter between them: how many were refused
+LOOPS = """
+#include "qlin.h"
+int loop_plan(int n, qlin_status (*f)(const int32_t*, int64_t, int64_t, void*, size_t, void*), const int32_t* ids,
+              int64_t M, int64_t L, void* plan, size_t bytes, void* stream)
+{
+    int bad = 0;
+    for (int i = 0; i < n; ++i)
+        bad += f(ids, M, L, plan, bytes, stream) != QLIN_OK;
+    return bad;
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def loops(tmp_path_factory):
+    at = tmp_path_factory.mktemp("loops")
+    (at / "loops.c").write_text(LOOPS)
+    subprocess.run(["gcc", "-O2", "-shared", "-fPIC", "-I", os.path.join(os.path.dirname(HERE), "include"),
+                    str(at / "loops.c"), "-o", str(at / "loops.so")], check=True)
+    return str(at / "loops.so")
+
+
 def run_fresh(script, threads):
     """In a process of its own, whose first calls of a kernel are these."""
     code = PRELUDE.format(here=HERE, root=os.path.dirname(HERE), threads=threads) + script
@@ -70,3 +93,30 @@ for case in ((BF, 24, 4096, 1024, 2, 128, "random"), (HF, 24, 4096, 1024, 2, 128
     assert all(torch.equal(a, b) for g in got for a, b in zip(g, got[0]))
     ref.check_forward(d["x"], d["a"], d["b"], d["scales"], d["ids"], d["base"], got[0][0], got[0][1])
 """, 8)
+
+
+def test_plans_for_pools_of_different_sizes(loops):
+    """Plans of 1024 adapters (131 KB of counters) beside plans of 2: no call takes another's shared memory away."""
+    run_fresh(f"""
+import ctypes as C
+loop, f = C.CDLL({loops!r}).loop_plan, C.cast(ql.lib().qlin_adapters_plan, C.c_void_p)
+gen = torch.Generator(device="cuda").manual_seed(3)
+M, pools = 64, (1024, 2)
+ids = [ref.make_ids("random", M, L, gen) for L in pools]
+want = [ql.adapters_plan(i, L).buffer for i, L in zip(ids, pools)]
+
+def body(j):
+    L, s = pools[j % 2], streams[j]
+    plan = torch.zeros_like(want[j % 2])
+    for _ in range(20):
+        gate.wait(60)
+        bad = loop(500, f, C.c_void_p(ids[j % 2].data_ptr()), C.c_int64(M), C.c_int64(L), C.c_void_p(plan.data_ptr()),
+                   C.c_size_t(plan.numel()), C.c_void_p(s.cuda_stream))
+        s.synchronize()
+        assert bad == 0, "calls refused: " + str(bad)
+    a, b = (t.view(torch.int32) for t in (plan, want[j % 2]))
+    n = 8 + 2 * ((L + 5) // 4 * 4)
+    assert torch.equal(a[8:8 + L + 2], b[8:8 + L + 2]) and torch.equal(a[n:n + M], b[n:n + M])
+
+at_once(body)
+""", 4)
