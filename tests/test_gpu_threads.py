@@ -120,3 +120,16 @@ def body(j):
 
 at_once(body)
 """, 4)
+
+
+@pytest.mark.parametrize("adapters", [300, 383])
+def test_first_plan_of_a_pool(adapters):
+    """Pools whose counters end about the shared memory that a kernel has without asking: 48 KB, less its own."""
+    run_fresh(f"""
+gen = torch.Generator(device="cuda").manual_seed(3)
+ids = ref.make_ids("random", 500, {adapters}, gen)
+plan = ql.adapters_plan(ids, {adapters})
+n = 8 + 2 * (({adapters} + 5) // 4 * 4)
+key = torch.where(ids < 0, {adapters}, ids.long())
+assert torch.equal(plan.buffer.view(torch.int32)[n:n + 500].long(), torch.sort(key, stable=True).indices)
+""", 1)
