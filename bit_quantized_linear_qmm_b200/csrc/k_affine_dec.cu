@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(W * 32, 1) affine_dec_kernel(const __grid_cons
 template <typename Kern>
 cudaError_t launch_dec(Kern kern, unsigned grid, int warps, int smem, cudaStream_t st, const DecParams& prm)
 {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_launch(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};

@@ -859,7 +859,7 @@ cudaError_t launch_pdl(Kern kern, dim3 grid, int smem, cudaStream_t st, const Pa
 {
     if (smem > 227 * 1024)
         return cudaErrorNotSupported;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_launch(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};

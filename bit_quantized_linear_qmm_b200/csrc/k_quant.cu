@@ -1169,8 +1169,7 @@ cudaError_t launch_quantize_weight_int8_clip(const void* w, qlin_dtype w_dt, int
     const size_t smem = (size_t)C * 4;  // the row's |w| bit patterns
     auto run = [&](auto* typed) {
         using TW = std::remove_const_t<std::remove_pointer_t<decltype(typed)>>;
-        cudaError_t e = cudaFuncSetAttribute(quantize_weight_int8_clip_kernel<TW>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaError_t e = allow_launch(reinterpret_cast<const void*>(quantize_weight_int8_clip_kernel<TW>), (int)smem);
         if (e != cudaSuccess)
             return e;
         quantize_weight_int8_clip_kernel<TW><<<(unsigned)R, 256, smem, st>>>(typed, C, pct, q, scale);

@@ -51,6 +51,25 @@ int loop_plan(int n, qlin_status (*f)(const int32_t*, int64_t, int64_t, void*, s
         bad += f(ids, M, L, plan, bytes, stream) != QLIN_OK;
     return bad;
 }
+int loop_matmul(int n, qlin_status (*f)(const void*, qlin_dtype, int64_t, int64_t, const uint32_t*, const void*,
+                                        const void*, qlin_dtype, int64_t, int, int, const void*, void*, void*, size_t,
+                                        void*),
+                const void* x, int64_t K, const uint32_t* codes, const void* scales, const void* biases, int64_t N, void* y,
+                void* ws, size_t bytes, void* stream)
+{
+    int bad = 0;
+    for (int i = 0; i < n; ++i)
+        bad += f(x, QLIN_BF16, 1, K, codes, scales, biases, QLIN_BF16, N, 4, 64, 0, y, ws, bytes, stream) != QLIN_OK;
+    return bad;
+}
+int loop_clip(int n, qlin_status (*f)(const void*, qlin_dtype, int64_t, int64_t, double, int8_t*, float*, void*),
+              const void* w, int64_t R, int64_t C, int8_t* q, float* scale, void* stream)
+{
+    int bad = 0;
+    for (int i = 0; i < n; ++i)
+        bad += f(w, QLIN_F32, R, C, 99.0, q, scale, stream) != QLIN_OK;
+    return bad;
+}
 """
 
 
@@ -119,6 +138,50 @@ def body(j):
     assert torch.equal(a[8:8 + L + 2], b[8:8 + L + 2]) and torch.equal(a[n:n + M], b[n:n + M])
 
 at_once(body)
+""", 4)
+
+
+def test_layers_of_different_sizes(loops):
+    """One decode kernel for a long and a short layer, and the clipping quantiser for long and short rows."""
+    run_fresh(f"""
+import ctypes as C
+lib, L = C.CDLL({loops!r}), ql.lib()
+P, I64 = C.c_void_p, C.c_int64
+ptr = lambda t: P(t.data_ptr())
+gen = torch.Generator(device="cuda").manual_seed(3)
+rn = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+layers = [(*ql.quantize(rn(N, K) * 0.05, 4, 64), rn(1, K).to(BF)) for N, K in ((8192, 8192), (256, 512))]
+rows = [rn(4, 16384), rn(4, 64)]
+
+def matmul(j, n):
+    codes, sc, bi, x = layers[j % 2]
+    y = torch.empty(1, codes.shape[0], dtype=BF, device="cuda")
+    ws = torch.empty(max(16, ql.workspace_size(ql.QLIN_OP_MATMUL, 1, y.shape[1], x.shape[1], 4, 64)), dtype=torch.uint8,
+                     device="cuda")
+    bad = lib.loop_matmul(n, C.cast(L.qlin_matmul, P), ptr(x), I64(x.shape[1]), ptr(codes), ptr(sc), ptr(bi),
+                          I64(y.shape[1]), ptr(y), ptr(ws), C.c_size_t(ws.numel()), P(streams[j].cuda_stream))
+    return y, bad
+
+def clip(j, n):
+    w = rows[j % 2]
+    q, s = torch.empty(w.shape, dtype=torch.int8, device="cuda"), torch.empty(4, device="cuda")
+    bad = lib.loop_clip(n, C.cast(L.qlin_quantize_weight_int8, P), ptr(w), I64(4), I64(w.shape[1]), ptr(q), ptr(s),
+                        P(streams[j].cuda_stream))
+    return q, bad
+
+for call in (matmul, clip):
+    torch.cuda.synchronize()
+    want = [call(i, 1)[0] for i in (0, 1)]
+
+    def body(j):
+        for _ in range(10):
+            gate.wait(60)
+            got, bad = call(j, 500)
+            streams[j].synchronize()
+            assert bad == 0, call.__name__ + " calls refused: " + str(bad)
+        assert torch.equal(got, want[j % 2])
+
+    at_once(body)
 """, 4)
 
 
