@@ -816,38 +816,41 @@ QLIN_DEV float amax16(const uint4 (&u)[2])
 }
 
 // The same with G/16 lanes per group, 16 consecutive values each (16-byte loads, one 16-byte store
-// of the lane's int8 codes); 16-byte aligned w and q.  A warp takes 8 rows by 512 columns, two rows at
+// of the lane's int8 codes); 16-byte aligned w and q.  A warp takes the most columns, 512 or a smaller
+// power of two, that divide K, and as many rows side by side as that leaves lanes for (a warp of 512
+// columns whatever K took 284 us for 1000000 rows of 64, where this takes 45).  A lane has two rows at
 // a time: lane l of a group divides for row l mod 2 and hands scale and reciprocal to the others, and
-// the 8 scales of a group fill one 32-byte sector.  16384 x 14336, g 128: 156 us, 4.6 TB/s for bf16
-// activations whose tokens differ in size; of normal values bf16 183, fp16 142, fp32 178 us (6.6 TB/s).
+// the scales of a group's rows are neighbours in memory.  16384 x 14336, g 128, normal values: bf16 156
+// us (4.6 TB/s), fp16 124 (5.8), fp32 171 (6.9, the copy rate).
 // The 16-bit types are bound by issue slots, bf16 most: its short significands meet half-integers more
 // often (4% of a lane's 16 values hold one, 1% in the activations).  A code is the low byte of
 // fma(x, r, 1.5 2^23), the product rounded half to even as rint does it.  With r = (1/s)(1 + e1) the
 // product and the rounded quotient q (1 + e3) differ by less than 2 2^-24 127 = 1.6e-5, so they round
 // alike unless the product lies within 3e-5 of a half-integer; such an element takes the division.
 template <typename TW, int G>
-__global__ void __launch_bounds__(256) quantize_int8_groups_vec_kernel(const TW* __restrict__ w, int64_t N, int64_t K,
-                                                                      int8_t* __restrict__ q,
-                                                                      float* __restrict__ scale_w, int rows_of_warp)
+__global__ void __launch_bounds__(32, sizeof(TW) == 4 ? 26 : 32)
+    quantize_int8_groups_vec_kernel(const TW* __restrict__ w, int64_t N, int64_t K, int8_t* __restrict__ q,
+                                    float* __restrict__ scale_w, int lanes_log2, int steps)
 {
     constexpr int LPG = G / 16;                     // lanes a group
     constexpr int NV = sizeof(TW) == 4 ? 4 : 2;     // 16-byte loads of 16 elements
-    constexpr int RPT = 2;                          // rows at a time (4: 185 us where 2 take 156)
+    constexpr int RPT = 2;                          // rows of a lane at a time
     const int lane = threadIdx.x & 31, first = lane & ~(LPG - 1), my = lane & (RPT - 1);
-    const int64_t col = (int64_t)blockIdx.x * 512 + 16 * lane;
-    const bool in = col < K;  // a group's lanes are all in or all out
-    const int64_t warps = blockDim.x >> 5, stride = gridDim.y * warps * rows_of_warp;
-    for (int64_t rows = ((int64_t)blockIdx.y * warps + (threadIdx.x >> 5)) * rows_of_warp; rows < N; rows += stride) {
+    const int slots = 32 >> lanes_log2, slot = lane >> lanes_log2;  // rows side by side in a warp
+    const int64_t col = (int64_t)blockIdx.x * (16 << lanes_log2) + 16 * (lane & ((1 << lanes_log2) - 1));
+    const int step = RPT * slots, rows_of_block = step * steps;
+    for (int64_t rows = (int64_t)blockIdx.y * rows_of_block; rows < N; rows += (int64_t)gridDim.y * rows_of_block) {
 #pragma unroll 1
-        for (int64_t n = rows; n < rows + rows_of_warp && n < N; n += RPT) {
+        for (int64_t n0 = rows; n0 < rows + rows_of_block && n0 < N; n0 += step) {
+            const int64_t n = n0 + RPT * slot;
             uint4 raw[RPT][NV];
             float amax[RPT];
 #pragma unroll
             for (int j = 0; j < RPT; ++j)
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
-                    raw[j][i] = in && n + j < N ? __ldg(reinterpret_cast<const uint4*>(w + (n + j) * K + col) + i)
-                                                : make_uint4(0u, 0u, 0u, 0u);
+                    raw[j][i] = n + j < N ? __ldg(reinterpret_cast<const uint4*>(w + (n + j) * K + col) + i)
+                                          : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
             for (int j = 0; j < RPT; ++j) {
                 if constexpr (sizeof(TW) == 4)
@@ -871,7 +874,7 @@ __global__ void __launch_bounds__(256) quantize_int8_groups_vec_kernel(const TW*
                 sc = 1.f;
             // a scale whose reciprocal is not normal: NaN, so that every element divides
             const float rsc = rcp_ok(sc) ? __frcp_rn(sc) : __uint_as_float(0x7fc00000u);
-            if (in && (lane & (LPG - 1)) < RPT && n + my < N)
+            if ((lane & (LPG - 1)) < RPT && n + my < N)
                 scale_w[(col / G) * N + n + my] = sc;
 #pragma unroll
             for (int j = 0; j < RPT; ++j) {
@@ -907,7 +910,7 @@ __global__ void __launch_bounds__(256) quantize_int8_groups_vec_kernel(const TW*
                                            ((uint32_t)sym_code(x, s, r, false) & 0xffu) << (8 * (i & 3));
                     }
                 }
-                if (in && n + j < N)
+                if (n + j < N)
                     *reinterpret_cast<uint4*>(q + (n + j) * K + col) = make_uint4(word[0], word[1], word[2], word[3]);
             }
         }
@@ -1187,18 +1190,21 @@ cudaError_t launch_quantize_int8_groups(const void* w, qlin_dtype w_dt, int64_t 
 {
     const bool vec = ((reinterpret_cast<uintptr_t>(w) | reinterpret_cast<uintptr_t>(q)) & 15u) == 0;
     const unsigned blocks = (unsigned)((N * (K / g) + 7) / 8);
-    // a block: 8 warps of 8 rows by 512 columns; where that is less than two blocks an SM, one warp of 4
-    // rows
-    const int64_t across = (K + 511) / 512;
-    const bool few = across * ((N + 63) / 64) < 2 * dev.sm_count;
-    const int rows = few ? 4 : 8, threads = few ? 32 : 256;
-    const int64_t down = few ? (N + 3) / 4 : (N + 63) / 64;
+    // A block is one warp.  Of 16-bit types it takes one step of rows up to 128 blocks an SM and two above:
+    // bf16 2048 x 4096 (8192 blocks) 8.9 us by one and 8.8 by two, 8192 x 4096 (32768) 25.8 and 25.4,
+    // 16384 x 14336 (229376) 160 and 151; 256 x 4096 3.7 and 5.0.  Of fp32 always one: 167 us and 168.
+    int lanes_log2 = 5;
+    while ((K >> 4 & ((int64_t(1) << lanes_log2) - 1)) != 0)
+        --lanes_log2;
+    const int64_t across = K >> (4 + lanes_log2), rows = int64_t(64) >> lanes_log2;
+    const int steps = w_dt != QLIN_F32 && across * ((N + rows - 1) / rows) > 128 * (int64_t)dev.sm_count ? 2 : 1;
+    const int64_t down = (N + rows * steps - 1) / (rows * steps);
     const dim3 vblocks((unsigned)across, (unsigned)(down < 65535 ? down : 65535));
 #define QLIN_QG(TW, G)                                                                                               \
     do {                                                                                                             \
         if (vec)                                                                                                     \
             quantize_int8_groups_vec_kernel<TW, G>                                                                   \
-                <<<vblocks, threads, 0, st>>>(static_cast<const TW*>(w), N, K, q, scale_w, rows);                    \
+                <<<vblocks, 32, 0, st>>>(static_cast<const TW*>(w), N, K, q, scale_w, lanes_log2, steps);            \
         else                                                                                                         \
             quantize_int8_groups_kernel<TW, G><<<blocks, 256, 0, st>>>(static_cast<const TW*>(w), N, K, q, scale_w); \
     } while (0)
