@@ -15,7 +15,8 @@
 // a gram step, longer than anything else in it).
 //
 // h, u and v enter their second product as two 16-bit halves, hi = round(h) and lo = round(h - hi):
-// 2^-16 of the value at most, and two MMAs instead of one.  They are kept in slots, [tile][128][Rq]
+// 2^-16 of the value at most (fp16: or 2^-39 of the largest under one scale, half of fp16's smallest
+// step, where that is more), and two MMAs instead of one.  They are kept in slots, [tile][128][Rq]
 // (Rq = R rounded up to 16), zero where there is no token or rank, hi and lo apart.  fp16 halves
 // are scaled by a power of two that puts the largest value of the row (wide) or of the adapter
 // (grams) in [2^14, 2^15), undone on the fp32 sum; bf16 has fp32's range and needs none.

@@ -370,9 +370,10 @@ size_t qlin_adapters_workspace_size(int64_t M, int64_t N, int64_t K, int64_t L, 
  * dtype dt, aligned to their elements.  plan: of the same M and L.
  * u: fp32 [M, R] or NULL: gets A_i x[m], zero without an adapter -- what the
  * backward pass needs.  1 <= R <= 128; K, N < 2^21 (QLIN_ERR_UNSUPPORTED
- * otherwise).  Accumulation in fp32, u split into two 16-bit halves (a
- * relative error of 2^-16 at most) for the second product, one rounding of
- * the sum to dt.  bf16 and fp16 with K and N multiples of 8, R of 4 and tensors
+ * otherwise).  Accumulation in fp32, u split into two 16-bit halves for the
+ * second product (an error of 2^-16 of its value at most; fp16: or 2^-39 of
+ * the largest |u| of the token, where that is more), one rounding of the sum
+ * to dt.  bf16 and fp16 with K and N multiples of 8, R of 4 and tensors
  * aligned to 16 bytes run on the tensor cores: few tokens in one launch, more
  * in two.  Everything else takes general fp32 kernels (slower).  workspace:
  * qlin_adapters_workspace_size(M, N, K, L, R, 0) bytes, 256-byte aligned.
@@ -395,9 +396,14 @@ qlin_status qlin_adapters_forward(const void* x, qlin_dtype dt, int64_t M, int64
  * qlin_quantize_int8_groups(x).  dx_base: [M, K], the gradient that the shared
  * projection passes on, or NULL (zeros); dx: [M, K], may be dx_base itself, or
  * NULL (not wanted).  da: [L, R, K], db: [L, N, R], written whole: zeros for
- * adapters without tokens.  All of dtype dt.  Sizes as forward; with a
- * checkpoint group_size in {64, 128, 256} and K % group_size == 0.  Sums over
- * tokens have a fixed order.  workspace:
+ * adapters without tokens.  All of dtype dt; a result beyond its range is
+ * infinite.  Sizes as forward; with a checkpoint group_size in {64, 128, 256}
+ * and K % group_size == 0.  Sums over tokens have a fixed order.  On the
+ * tensor cores u and v enter their second product as halves, as u does in
+ * forward (fp16: 2^-39 of the largest of the token for dx, of the adapter for
+ * da and db), and an input restored from its checkpoint is rounded once to dt,
+ * as qlin_dequantize_int8_groups would (fp16: infinite above 65504, which a
+ * checkpoint of bf16 or fp32 inputs can hold).  workspace:
  * qlin_adapters_workspace_size(M, N, K, L, R, 1) bytes, 256-byte aligned.
  */
 qlin_status qlin_adapters_backward(const void* dy, qlin_dtype dt, int64_t M, int64_t N, const void* a, const void* b,
@@ -424,7 +430,8 @@ qlin_status qlin_dequantize_int8_groups(const int8_t* q, const float* scale, int
  * dy: [M, N] of dt, bf16 or fp16 (QLIN_ERR_UNSUPPORTED for fp32); q: int8
  * [M, K], scale: fp32 [K/group_size, M]; dw: [N, K], db: [N] of dt, written
  * whole.  Each restored input is rounded once to dt as the tensor cores'
- * operand; sums in fp32 in a fixed order, one rounding to dt.  N % 8 == 0,
+ * operand (fp16: infinite above 65504, which a checkpoint of bf16 or fp32
+ * inputs can hold); sums in fp32 in a fixed order, one rounding to dt.  N % 8 == 0,
  * dy, q and dw 16-byte aligned (QLIN_ERR_MISALIGNED); group_size in
  * {64, 128, 256}, K % group_size == 0, K < 2^21.
  */
