@@ -141,6 +141,9 @@ qlin_status from_cuda(cudaError_t e)
 bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
 bool int8_group_ok(int g) { return g == 64 || g == 128 || g == 256; }
 constexpr int64_t kMaxFeatures = 1 << 21;  // K, N of the adapter calls and of wgrad: block counts of a grid
+// Tokens of a weight gradient: fp32 sums of as many terms of one size still grow, and a tile of them (1.44
+// us a stage of 64) takes 0.4 s, where a wait for its sums gives up after 2 s.
+constexpr int64_t kMaxWgradTokens = 1 << 24;
 
 // Sizes of the adapter calls: INVALID_ARG below 1, UNSUPPORTED above what the kernels hold.
 qlin_status check_plan(int64_t M, int64_t L)
@@ -721,7 +724,8 @@ qlin_status pergroup_wgrad(const void* dy, qlin_dtype dt, int64_t M, int64_t N, 
 {
     if (!dy || !q || !scale || !dw || M <= 0 || N <= 0 || K <= 0 || M > INT32_MAX)
         return QLIN_ERR_INVALID_ARG;
-    if ((dt != QLIN_BF16 && dt != QLIN_F16) || !int8_group_ok(group_size) || N >= kMaxFeatures || K >= kMaxFeatures)
+    if ((dt != QLIN_BF16 && dt != QLIN_F16) || !int8_group_ok(group_size) || N >= kMaxFeatures || K >= kMaxFeatures ||
+        M > kMaxWgradTokens)
         return QLIN_ERR_UNSUPPORTED;
     if (K % group_size != 0)
         return QLIN_ERR_INVALID_ARG;

@@ -433,7 +433,8 @@ qlin_status qlin_dequantize_int8_groups(const int8_t* q, const float* scale, int
  * operand (fp16: infinite above 65504, which a checkpoint of bf16 or fp32
  * inputs can hold); sums in fp32 in a fixed order, one rounding to dt.  N % 8 == 0,
  * dy, q and dw 16-byte aligned (QLIN_ERR_MISALIGNED); group_size in
- * {64, 128, 256}, K % group_size == 0, K < 2^21.
+ * {64, 128, 256}, K % group_size == 0, N and K < 2^21, M <= 2^24 (a longer
+ * batch in parts; QLIN_ERR_UNSUPPORTED).
  */
 qlin_status pergroup_wgrad(const void* dy, qlin_dtype dt, int64_t M, int64_t N, const int8_t* q, const float* scale,
                            int64_t K, int group_size, void* dw, void* db, void* stream);

@@ -48,3 +48,20 @@ def test_many_tiles(ql, case):
         ref.close(dw[:, p], yd.T @ xh[:, p], (ref.half(dt) + ref.acc(M)) * (yd.abs().T @ xh[:, p].abs()), f"dw from {c}")
     again, b2 = ql.pergroup_wgrad(dy, q, s, g)
     assert torch.equal(again, dw) and torch.equal(b2, db)
+
+
+@pytest.mark.parametrize("N,K", [(8, 64), (264, 256)])
+def test_the_longest_batch(ql, N, K):
+    """2^24 tokens (one CTA a tile, and a pair), codes and gradients of -1, 0 and 1: the sums are whole numbers below
+    2^24, exact in fp32, whatever their order."""
+    M, g = 1 << 24, 64
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.randint(-1, 2, (M, K), generator=gen, device="cuda", dtype=torch.int8)
+    dy = torch.randint(-1, 2, (M, N), generator=gen, device="cuda", dtype=torch.int8).to(BF)
+    s = torch.ones(K // g, M, device="cuda")
+    dw, db = ql.pergroup_wgrad(dy, q, s, g)
+    assert ql.device_status() == ql.QLIN_OK
+    want, sums = torch.zeros(N, K, dtype=torch.float64, device="cuda"), dy.sum(0, dtype=torch.float64)
+    for m in range(0, M, 1 << 20):
+        want += dy[m:m + (1 << 20)].double().T @ q[m:m + (1 << 20)].double()
+    assert torch.equal(dw, want.to(BF)) and torch.equal(db, sums.to(BF))
