@@ -1,6 +1,7 @@
 // qlin_abi.cu -- the extern "C" boundary of libqlin.so: argument validation,
 // device checks, workspace sizing and dispatch to the kernel launchers.
 // No exception crosses this file's functions; every failure is a qlin_status.
+#include <initializer_list>
 #include <mutex>
 
 #include "adapters.cuh"
@@ -177,6 +178,23 @@ bool overlap(const void* p, size_t pn, const void* q, size_t qn)
 {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
     return p && q && a < b + qn && b < a + pn;
+}
+struct Span {
+    const void* p;  // null: not given
+    size_t n;
+};
+// Nothing that a call writes lies over anything it reads, or over anything else it writes.
+bool apart(std::initializer_list<Span> written, std::initializer_list<Span> read)
+{
+    for (const Span* w = written.begin(); w != written.end(); ++w) {
+        for (const Span* o = written.begin(); o != w; ++o)
+            if (overlap(w->p, w->n, o->p, o->n))
+                return false;
+        for (const Span& r : read)
+            if (overlap(w->p, w->n, r.p, r.n))
+                return false;
+    }
+    return true;
 }
 
 // Shape/type rules common to the affine-format calls.
@@ -628,6 +646,8 @@ qlin_status qlin_adapters_plan(const int32_t* ids, int64_t M, int64_t L, void* p
     DeviceInfo dev;
     if ((s = current_device(dev)) != QLIN_OK)
         return s;
+    if (!apart({{plan, qlin_adapters_plan_size(M, L)}}, {{ids, (size_t)M * 4}}))
+        return QLIN_ERR_INVALID_ARG;
     return from_cuda(launch_adapters_plan(ids, M, L, plan, static_cast<cudaStream_t>(stream)));
 }
 
@@ -650,17 +670,21 @@ qlin_status qlin_adapters_forward(const void* x, qlin_dtype dt, int64_t M, int64
     qlin_status s = check_adapters(dt, M, N, K, L, R, plan, plan_bytes);
     if (s != QLIN_OK)
         return s;
-    const size_t e = dtype_size(dt), xn = M * K * e, on = M * N * e;
+    const size_t e = dtype_size(dt), on = M * N * e, ws_need = qlin_adapters_workspace_size(M, N, K, L, R, 0);
     if (!aligned_to(e, x, a, b, base, out) || !aligned_to(4, scales, u))
         return QLIN_ERR_MISALIGNED;
-    if (overlap(out, on, x, xn) || (base != out && overlap(out, on, base, on)) ||
-        overlap(u, (size_t)M * R * 4, out, on))
+    const Span out_s = {out, on}, u_s = {u, (size_t)(M * R) * 4}, x_s = {x, M * K * e}, a_s = {a, L * R * K * e},
+               b_s = {b, L * N * R * e}, sc_s = {scales, (size_t)L * 4}, base_s = {base == out ? nullptr : base, on},
+               plan_s = {plan, qlin_adapters_plan_size(M, L)};
+    if (!apart({out_s, u_s}, {x_s, a_s, b_s, sc_s, base_s, plan_s}))
         return QLIN_ERR_INVALID_ARG;
-    if (!workspace || ws_bytes < qlin_adapters_workspace_size(M, N, K, L, R, 0) || !aligned256(workspace))
+    if (!workspace || ws_bytes < ws_need || !aligned256(workspace))
         return QLIN_ERR_WORKSPACE;
     DeviceInfo dev;
     if ((s = current_device(dev)) != QLIN_OK)
         return s;
+    if (!apart({{workspace, ws_need}}, {out_s, u_s, x_s, a_s, b_s, sc_s, base_s, plan_s}))
+        return QLIN_ERR_INVALID_ARG;
     const AdapterFwdArgs f = {x, a, b, scales, base, out, u, dt, M, K, N, L, R, plan_view(plan, M, L), workspace};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return from_cuda(adapters_tc_takes(f) ? launch_adapters_forward_tc(f, st, dev) : launch_adapters_forward_simt(f, st));
@@ -681,17 +705,24 @@ qlin_status qlin_adapters_backward(const void* dy, qlin_dtype dt, int64_t M, int
         return QLIN_ERR_UNSUPPORTED;
     if (q && K % group_size != 0)
         return QLIN_ERR_INVALID_ARG;
-    const size_t e = dtype_size(dt), xn = M * K * e, yn = M * N * e;
+    const size_t e = dtype_size(dt), xn = M * K * e, an = L * R * K * e, bn = L * N * R * e,
+                 ws_need = qlin_adapters_workspace_size(M, N, K, L, R, 1);
     if (!aligned_to(e, dy, a, b, x, dx_base, dx, da, db) || !aligned_to(4, scales, u, q_scale))
         return QLIN_ERR_MISALIGNED;
-    if (overlap(dx, xn, dy, yn) || overlap(dx, xn, x, xn) || overlap(dx, xn, q, (size_t)M * K) ||
-        (dx_base != dx && overlap(dx, xn, dx_base, xn)))
+    const Span dx_s = {dx, xn}, dy_s = {dy, M * N * e}, a_s = {a, an}, b_s = {b, bn}, sc_s = {scales, (size_t)L * 4},
+               u_s = {u, (size_t)(M * R) * 4}, x_s = {x, xn}, q_s = {q, (size_t)(M * K)},
+               qs_s = {q ? q_scale : nullptr, q ? (size_t)(K / group_size * M) * 4 : 0},
+               base_s = {dx_base == dx ? nullptr : dx_base, xn}, plan_s = {plan, qlin_adapters_plan_size(M, L)};
+    if (!apart({dx_s}, {dy_s, a_s, b_s, sc_s, u_s, x_s, q_s, qs_s, base_s, plan_s}))
         return QLIN_ERR_INVALID_ARG;
-    if (!workspace || ws_bytes < qlin_adapters_workspace_size(M, N, K, L, R, 1) || !aligned256(workspace))
+    if (!workspace || ws_bytes < ws_need || !aligned256(workspace))
         return QLIN_ERR_WORKSPACE;
     DeviceInfo dev;
     if ((s = current_device(dev)) != QLIN_OK)
         return s;
+    if (!apart({{da, an}, {db, bn}, {workspace, ws_need}, dx_s},
+               {dy_s, a_s, b_s, sc_s, u_s, x_s, q_s, qs_s, base_s, plan_s}))
+        return QLIN_ERR_INVALID_ARG;
     const AdapterBwdArgs g = {dy, a,  b,  scales, u,  x, q, q_scale, group_size, dx_base,
                               dx, da, db, dt,     M,  K, N, L,       R,          plan_view(plan, M, L),
                               workspace};
@@ -715,6 +746,8 @@ qlin_status qlin_dequantize_int8_groups(const int8_t* q, const float* scale, int
     qlin_status s;
     if ((s = current_device(dev)) != QLIN_OK)
         return s;
+    if (!apart({{out, N * K * dtype_size(out_dt)}}, {{q, (size_t)(N * K)}, {scale, (size_t)(K / group_size * N) * 4}}))
+        return QLIN_ERR_INVALID_ARG;
     return from_cuda(launch_dequantize_int8_groups(q, scale, N, K, group_size, out, out_dt,
                                                    static_cast<cudaStream_t>(stream)));
 }
@@ -736,6 +769,9 @@ qlin_status pergroup_wgrad(const void* dy, qlin_dtype dt, int64_t M, int64_t N, 
     qlin_status s;
     if ((s = current_device(dev)) != QLIN_OK)
         return s;
+    if (!apart({{dw, (size_t)(N * K) * 2}, {db, (size_t)N * 2}},
+               {{dy, (size_t)(M * N) * 2}, {q, (size_t)(M * K)}, {scale, (size_t)(K / group_size * M) * 4}}))
+        return QLIN_ERR_INVALID_ARG;
     return from_cuda(launch_pergroup_wgrad(dy, dt, M, N, q, scale, K, group_size, dw, db,
                                            static_cast<cudaStream_t>(stream), dev));
 }

@@ -366,8 +366,9 @@ size_t qlin_adapters_workspace_size(int64_t M, int64_t N, int64_t K, int64_t L, 
  * Adapters, forward.  x: [M, K]; a: [L, R, K] and b: [L, N, R], the factors of
  * every adapter (a rank below R: zero rows of a_i, zero columns of b_i);
  * scales: fp32 [L]; base: [M, N] or NULL (zeros); out: [M, N], may be base
- * itself (no other overlap: QLIN_ERR_INVALID_ARG for out over x or u); all of
- * dtype dt, aligned to their elements.  plan: of the same M and L.
+ * itself; all of dtype dt, aligned to their elements.  Otherwise nothing that
+ * this or the calls below write (outputs and workspace) may lie over anything
+ * they read or over one another: QLIN_ERR_INVALID_ARG.  plan: of the same M and L.
  * u: fp32 [M, R] or NULL: gets A_i x[m], zero without an adapter -- what the
  * backward pass needs.  1 <= R <= 128; K, N < 2^21 (QLIN_ERR_UNSUPPORTED
  * otherwise).  Accumulation in fp32, u split into two 16-bit halves for the
