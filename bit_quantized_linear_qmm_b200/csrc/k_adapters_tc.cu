@@ -994,6 +994,7 @@ struct GramParams {
     void* db;  // [L][N][R]
     int parts;  // CTAs of a tile in the narrow kernel: maxima of a tile
     int tmem_cols, room;  // room: bytes of shared memory for the rings
+    int z;                // CTAs of a cluster
 };
 
 template <typename T>
@@ -1007,10 +1008,10 @@ __global__ void __launch_bounds__(kGramThreads, 1) adapters_gram_kernel(const __
     __shared__ int abort_flag;
     const Common& c = p.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int z = gridDim.x, rank = blockIdx.x;
+    const int z = p.z, rank = blockIdx.x % z, job = blockIdx.x / z;
     pdl_wait_prior_grids();
     const int strips = p.strips_y + p.strips_x;
-    const int i = blockIdx.y / strips, strip = blockIdx.y % strips;
+    const int i = job / strips, strip = job % strips;
     const bool of_dy = strip < p.strips_y, of_q = !of_dy && p.q_scale;
     const int64_t n0 = (int64_t)(of_dy ? strip : strip - p.strips_y) * 256, ncols = of_dy ? p.N : p.K;
     const int seg0 = c.plan.seg[i], tokens = c.plan.seg[i + 1] - seg0, tile0 = c.plan.tile_l0[i];
@@ -1550,7 +1551,8 @@ cudaError_t launch_grams(const Common& c, const AdapterBwdArgs& a, const RowMaps
     int z = 1;
     while (z < kMaxGramSplit && jobs <= (z == 1 ? 72 : z == 2 ? 32 : 16) && c.M / c.L / 64 >= 4 * z)
         z *= 2;
-    return launch(adapters_gram_kernel<T>, dim3((unsigned)z, (unsigned)jobs), kGramThreads, p.room + 1024, z, p, st);
+    p.z = z;
+    return launch(adapters_gram_kernel<T>, dim3((unsigned)(z * jobs)), kGramThreads, p.room + 1024, z, p, st);
 }
 
 // Whether the one-launch kernel is faster than the two tensor-memory ones, by what both cost in us.
@@ -1657,22 +1659,21 @@ cudaError_t backward_t(const AdapterBwdArgs& a, cudaStream_t st, const DeviceInf
     return e;
 }
 
-bool tc_sizes(qlin_dtype dt, int64_t M, int64_t N, int64_t K, int64_t L, int64_t R)
+static_assert(kMaxPlanTokens / kTileL + kMaxAdapters + 1 <= 65535, "the tile list is a grid's y");
+bool tc_sizes(qlin_dtype dt, int64_t N, int64_t K, int64_t R)
 {
-    // the tile list and the gram jobs are a grid's y
-    return dt != QLIN_F32 && R % 4 == 0 && K % 8 == 0 && N % 8 == 0 && max_tiles(M, L, kTileL) <= 65535 &&
-           L * ((N + 255) / 256 + (K + 255) / 256) <= 65535;
+    return dt != QLIN_F32 && R % 4 == 0 && K % 8 == 0 && N % 8 == 0;
 }
 
 }  // namespace
 
 bool adapters_tc_takes(const AdapterFwdArgs& a)
 {
-    return tc_sizes(a.dt, a.M, a.N, a.K, a.L, a.R) && a16({a.x, a.a, a.b, a.base, a.out, a.u});
+    return tc_sizes(a.dt, a.N, a.K, a.R) && a16({a.x, a.a, a.b, a.base, a.out, a.u});
 }
 bool adapters_tc_takes(const AdapterBwdArgs& a)
 {
-    return tc_sizes(a.dt, a.M, a.N, a.K, a.L, a.R) &&
+    return tc_sizes(a.dt, a.N, a.K, a.R) &&
            a16({a.dy, a.a, a.b, a.u, a.x, a.q, a.dx_base, a.dx, a.da, a.db});
 }
 
