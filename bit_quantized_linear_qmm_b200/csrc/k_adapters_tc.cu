@@ -1383,7 +1383,7 @@ struct Layout {
         back = up256(slots * sizeof(float));
         v = up256(slots * (size_t)rank_up(R) * sizeof(float));
         tile_max = up256(tiles * kMaxSplit * 2 * sizeof(float));
-        pad = R % 8 ? up256((size_t)L * (size_t)N * (size_t)(R + 4) * 2) : 0;
+        pad = R % 8 == 4 ? up256((size_t)L * (size_t)N * (size_t)(R + 4) * 2) : 0;
         total = 3 * halves + back + v + tile_max + pad;
     }
 };
