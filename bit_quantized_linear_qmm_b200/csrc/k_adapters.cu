@@ -20,7 +20,9 @@ namespace {
 
 // One CTA of 32 warps; warp w counts, then places, the tokens of the w-th part of the batch in
 // order, so tokens of one adapter stay ascending (and sums over them have a fixed order).  Lanes
-// with the same adapter are grouped by match_any; no atomics.
+// with the same adapter are grouped by match_any; no atomics.  One CTA, since batches are short and the
+// plan is made once for all layers: 61 tokens of 32 adapters 4.1 us, 4096 of 4 5.2 us, 4096 of 1024 17.7 us,
+// 65536 of 64 129 us, 2^20 of 1024 2.5 ms.
 __global__ void __launch_bounds__(1024) adapters_plan_kernel(const int32_t* __restrict__ ids, int M, int L, PlanView v)
 {
     extern __shared__ int cnt[];  // [32][L + 1]
