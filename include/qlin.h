@@ -349,7 +349,8 @@ qlin_status w8a8_linear_noalloc(const void* x, qlin_dtype x_dt, int64_t M, int64
  * qlin_adapters_plan orders the tokens of a batch by adapter.  A plan depends
  * on ids alone: one serves every layer of a model, forward and backward, until
  * the batch changes.  ids: int32 [M] on the device, in any order; plan:
- * qlin_adapters_plan_size(M, L) bytes, 16-byte aligned, written whole.
+ * qlin_adapters_plan_size(M, L) bytes, 16-byte aligned, written whole, not
+ * over ids.
  * 1 <= M <= 2^20, 1 <= L <= 1024 (QLIN_ERR_UNSUPPORTED above).
  * qlin_adapters_plan_size gives 0 for sizes outside these.
  */

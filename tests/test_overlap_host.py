@@ -2,6 +2,7 @@
 import ctypes as C
 
 import pytest
+import torch
 
 from helpers import build_lib
 
@@ -52,6 +53,7 @@ def test_backward(ql, k):
     assert backward(ql, **k) == ql.QLIN_ERR_INVALID_ARG
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="these calls would be launched, at addresses of nothing")
 def test_buffers_that_touch_are_apart(ql):
     fine = forward(ql)
     assert fine != ql.QLIN_ERR_INVALID_ARG
