@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(256) dequantize_int8_groups_kernel(const int8_
 // freed once the MMAs in flight are done.
 // The restored inputs are rounded to the operand's type because the tensor cores multiply two of one
 // 16-bit type; holding them in two terms would double the MMAs that bound the long batches.  Of [14336]
-// [4096] in bf16 dW is off by 0.0020 of its norm, of which 0.0017 is the result's own rounding (fp16 0.00023
+// [4096] in bf16 dW is off by 0.0020 of its norm, of which 0.0017 is the result's own rounding (fp16 0.00024
 // and 0.00021).
 // dW [14336][4096] of 4096 tokens: 406 - 432 us in bursts of five calls, 447 in a loop of 3 s at 1.6 GHz
 // under the power cap, 1.18 - 1.08 PFLOP/s (single CTAs on 256 x 256 tiles: 501 and more); [4096][11008]
